@@ -118,7 +118,9 @@ typedef enum {
     SA_OP_DENSE = 3,     /* sa_dense_decode  */
     SA_OP_STEP = 4,      /* sa_step          */
     SA_OP_MULTI = 5,     /* sa_multi_step    */
-    SA_OP_CLUSTER = 6    /* sa_cluster_build */
+    SA_OP_CLUSTER = 6,   /* sa_cluster_build */
+    SA_OP_PAGED_DECODE = 7, /* sa_paged_decode (sa_paged_workspace_size) */
+    SA_OP_PAGED_EVICT = 8   /* sa_paged_evict  (sa_paged_workspace_size) */
 } sa_op;
 
 /* Supported: d in {64, 128}; Hq % Hkv == 0 with G = Hq/Hkv in {1,2,4,8};
@@ -447,6 +449,128 @@ SA_API sa_status sa_multi_step(const sa_shape* shape, const void* q, const void*
  * part of the method): out [B, Hq, d] f32 = softmax(s q K^T) V. */
 SA_API sa_status sa_dense_decode(const sa_shape* shape, const void* q, const void* k, const void* v,
                           float* out, float scale, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- the paged cache ---------------------------------------------------------
+ *
+ * Sequences of unequal lengths in one pool of pages: row b of `table` lists
+ * the pages of sequence b, and slot s of the sequence is row s % page of page
+ * table[b, s / page].  A slot's position is the index of its token in the
+ * sequence; eviction moves tokens between slots, and `pos` then says which
+ * token a slot holds.  Lengths, tables and positions are read on the device
+ * by each call, so a call captured in a CUDA graph follows them at replay.
+ * The method has no counterpart: these are the dense operators a serving
+ * program needs beside the sparse ones.
+ *
+ * Supported: d in {64, 128}; any Hq / Hkv; any page size; B * Hkv < 65536,
+ * B * Hq < 2^24, max_pages * page <= 2^30 (the capacity in slots of a
+ * sequence, `cap` below); fewer than 2^31 64-slot tiles in all.  Strides are
+ * in elements of dtype, positive multiples of 16 bytes; a row's d elements
+ * are contiguous; 0 for all three = the dense pool
+ * [n_pages, Hkv, page, d] (row_stride d, head_stride page d, page_stride
+ * Hkv page d).  k and v share the strides.  Token-major pools
+ * [n_pages, page, Hkv, d] have row_stride Hkv d, head_stride d. */
+typedef struct {
+    int B, Hq, Hkv, d;
+    sa_dtype dtype;
+    int n_pages, page, max_pages;   /* pages of the pool, tokens per page, columns of the table */
+    int ldw;                        /* slots per row of pos and of the weights (0 = cap; >= cap) */
+    long long page_stride, head_stride, row_stride;
+} sa_paged_shape;
+
+/*   k, v     the pools
+ *   table    [B, max_pages] int32; an entry that a length reaches and that is
+ *            not a page of the pool (outside [0, n_pages)) names no memory:
+ *            its slots are not written, and masked when read
+ *   lengths  [B] int32: tokens in the cache, in slots [0, lengths[b]); clamped
+ *            to [0, cap] by every call
+ *   pos      [B, Hkv, ldw] int32 or NULL: the position of the token in each
+ *            slot; NULL = slot s holds position s
+ *   seen     [B] int32 or NULL, given with pos and only with it: tokens the
+ *            sequence ever had, so that its newest position is seen[b] - 1
+ *            (without: lengths[b] - 1) */
+typedef struct {
+    void* k;
+    void* v;
+    const int32_t* table;
+    const int32_t* lengths;
+    int32_t* pos;
+    const int32_t* seen;
+} sa_paged_cache;
+
+/*   scale       softmax scale (0 = 1/sqrt(d))
+ *   softcap     c > 0: logits capped to c tanh(scale q.k / c); 0: not capped
+ *   sink, local with local > 0 a slot is visible when its position is one of
+ *               the first `sink` or the last `local` (position > newest -
+ *               local); local = 0: every slot
+ *   slopes      [Hq] f32 or NULL: slope_h (newest - position) is subtracted
+ *               from the (capped) logit
+ *   weight, weight_out  [B, Hkv, ldw] f32, weight_out NULL or the weights
+ *               accumulated over steps: for every slot s < lengths[b],
+ *               weight_out[b, g, s] = weight[b, g, s] + sum over the heads h
+ *               of group g of the attention weight p_hs of this step (weight
+ *               NULL = 0; the two may be the same array).  Slots past the
+ *               length are left as they were
+ *   q_stride    elements between the queries of two sequences (0 = Hq d; a
+ *               multiple of 16 bytes); the Hq heads of one are dense */
+typedef struct {
+    float scale, softcap;
+    int sink, local;
+    const float* slopes;
+    const float* weight;
+    float* weight_out;
+    long long q_stride;
+} sa_paged_params;
+
+/* Bytes of scratch of sa_paged_decode (arg != 0: with weight_out) or
+ * sa_paged_evict (arg = budget).  0 on invalid arguments.  Of the decode's only
+ * the first 4 B Hkv ceil(Hq / (8 Hkv)) bytes (the completion tickets) have to
+ * be zero when it is first used; the eviction's need not be.  A workspace
+ * serves one shape and one call at a time: calls that may run side by side
+ * (two streams, two captured graphs) take one each. */
+SA_API size_t sa_paged_workspace_size(const sa_paged_shape* shape, int op, int arg);
+
+/* Writes the newest tokens of the sequences into their slots.  The n_new
+ * tokens are packed: token i belongs to the sequence b with start[b] <= i <
+ * start[b + 1] (start [B + 1] int32, not decreasing; NULL: n_new = B, one
+ * each), its key and value heads at k_new / v_new + i token_stride + g
+ * head_stride (elements, multiples of 16 bytes; 0 for both = dense
+ * [n_new, Hkv, d]; n_new Hkv < 2^31).  The lengths (and seen) already count the new tokens: the
+ * n_b of sequence b are its last, slots lengths[b] - n_b + i, positions
+ * seen[b] - n_b + i.  pos (when not NULL) and weight (when not NULL,
+ * [B, Hkv, ldw] f32: set to 0) of those slots are written for every head.
+ * Tokens outside [start[0], start[B]), slots outside [0, cap) and pages
+ * outside the pool are skipped.  No workspace; one kernel. */
+SA_API sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cache* cache, const void* k_new,
+                                 const void* v_new, long long token_stride, long long head_stride,
+                                 const int32_t* start, int n_new, float* weight, void* stream);
+
+/* Attention of one query per sequence over its slots:
+ *   x_hs = cap(scale q_h . k_s) - slope_h (newest - pos_s),
+ *   lse[b, h] = ln sum_s exp(x_hs),  out[b, h, :] = sum_s exp(x_hs - lse) v_s
+ * over the visible slots (out [B, Hq, d] f32, lse [B, Hq] f32 or NULL).  A
+ * row that sees nothing (length 0, a window that leaves none, no valid page)
+ * gives out = 0, lse = -inf and adds no weight.  q [B, Hq, d] in dtype. */
+SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cache,
+                                 const sa_paged_params* params, const void* q, float* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* Thins every sequence with more than `budget` tokens out to `budget`, per KV
+ * head: the tokens of the first `sink` and the last `local` positions stay
+ * (sink + local <= budget), then the largest weights (weight [B, Hkv, ldw]
+ * f32; NaN counts as -inf), ties to the lower slot (should more slots than
+ * budget claim protected positions, the largest weights among those).  The i-th kept slot at or
+ * past the new length moves, key and value rows in place, into the i-th freed
+ * slot before it; the other kept slots stay where they are.  Written for
+ * every sequence: lengths_out [B] = min(lengths[b], budget), and for slots s <
+ * lengths_out[b] the weights and positions of the tokens now there
+ * (weight_out f32, pos_out int32, both [B, Hkv, ldw]; past it they are left as
+ * they were).  The outputs are other arrays than the inputs: repeating a call
+ * on the same inputs gives the same result.  A sequence's pages must be its
+ * own, each in one place of the table: rows are moved in place.  Pass the
+ * outputs as the cache's lengths, pos and weights from then on. */
+SA_API sa_status sa_paged_evict(const sa_paged_shape* shape, const sa_paged_cache* cache, const float* weight,
+                                int budget, int sink, int local, int32_t* lengths_out, float* weight_out,
+                                int32_t* pos_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Bounded waits.  The selection kernel streams the block summaries into
    shared memory with bulk copies and waits on each one for at most about two

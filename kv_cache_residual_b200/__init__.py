@@ -27,7 +27,7 @@ SA_F32, SA_BF16 = 0, 1
 MODES = {"drop": 0, "resa": 1, "proxy": 2, "sample": 3}
 SCORES = {"mean_sum": 0, "mean_max": 1, "quest": 2}
 BUDGETS = {"clt": 0, "clt_search": 1, "hoeffding": 2}
-OP_PREFILL, OP_SELECT, OP_DECODE, OP_DENSE, OP_STEP, OP_MULTI, OP_CLUSTER = range(7)
+OP_PREFILL, OP_SELECT, OP_DECODE, OP_DENSE, OP_STEP, OP_MULTI, OP_CLUSTER, OP_PAGED_DECODE, OP_PAGED_EVICT = range(9)
 
 
 class SAError(RuntimeError):
@@ -69,11 +69,27 @@ class sa_decode_params(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int), ("lam", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
+class sa_paged_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "d", "dtype", "n_pages", "page", "max_pages", "ldw")] + \
+               [(n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "row_stride")]
+
+
+class sa_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "lengths", "pos", "seen")]
+
+
+class sa_paged_params(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("sink", ctypes.c_int),
+                ("local", ctypes.c_int), ("slopes", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("weight_out", ctypes.c_void_p), ("q_stride", ctypes.c_longlong)]
+
+
 EXPORTS = ("sa_workspace_size", "sa_prefill_stats", "sa_block_summaries", "sa_block_sketch", "sa_block_minmax",
            "sa_select",
            "sa_select_noalloc",
            "sa_decode", "sa_step", "sa_dense_decode", "sa_append", "sa_wait_timeouts", "sa_cluster_prep", "sa_cluster_build",
            "sa_multi_step",
+           "sa_paged_workspace_size", "sa_paged_append", "sa_paged_decode", "sa_paged_evict",
            "sa_status_string")
 
 _LIB = None
@@ -105,6 +121,14 @@ def _lib():
         lib.sa_cluster_prep.argtypes = [sh, P, P, cl, P]
         lib.sa_cluster_build.argtypes = [sh, P, P, P, cl, I, P, S, P]
         lib.sa_multi_step.argtypes = [sh, P, P, P, cl, I, F, P, P, P, P, S, P]
+        psh, pc, L = ctypes.POINTER(sa_paged_shape), ctypes.POINTER(sa_paged_cache), ctypes.c_longlong
+        lib.sa_paged_workspace_size.argtypes = [psh, I, I]
+        lib.sa_paged_workspace_size.restype = S
+        lib.sa_paged_append.argtypes = [psh, pc, P, P, L, L, P, I, P, P]
+        lib.sa_paged_decode.argtypes = [psh, pc, ctypes.POINTER(sa_paged_params), P, P, P, P, S, P]
+        lib.sa_paged_evict.argtypes = [psh, pc, P, I, I, I, P, P, P, P, S, P]
+        for f in ("sa_paged_append", "sa_paged_decode", "sa_paged_evict"):
+            getattr(lib, f).restype = I
         lib.sa_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
         lib.sa_wait_timeouts.restype = I
         lib.sa_status_string.argtypes = [I]
@@ -461,6 +485,223 @@ def append(k_new, v_new, k, v, stats, length, scale=0.0, stream=None):
     _check(_lib().sa_append(ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _ptr(k), _ptr(v), ctypes.byref(st),
                             float(scale), _stream(stream)), "sa_append")
     return int(length) + 1
+
+
+# ---- the paged cache -----------------------------------------------------------
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this type, shape and device."""
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
+          "%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+    return t.data_ptr()
+
+
+class PagedCache:
+    """A cache of sequences of unequal lengths in one pool of pages (layouts of
+    sa_paged_shape and sa_paged_cache in sa_decode.h), for paged_append,
+    paged_decode and paged_evict.
+
+    k, v [n_pages, Hkv, page, d], bf16 or fp32, with any strides whose rows are
+    contiguous (a token-major pool [n_pages, page, Hkv, d] is passed as its
+    transpose(1, 2), a slice of a pool that holds both as that slice); table
+    [B, max_pages] and lengths [B] int32; pos [B, Hkv, max_pages * page] int32
+    and seen [B] int32 together, or neither (no token has been evicted).
+
+    The object holds the tensors and reads nothing from them: their values may
+    change between calls, and between replays of a captured one."""
+
+    def __init__(self, k, v, table, lengths, pos=None, seen=None):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device and k.is_cuda,
+              "k and v must be CUDA tensors [n_pages, Hkv, page, d] of one type, shape and device")
+        _need(table.dim() == 2, "table must be [B, max_pages]")
+        self.n_pages, self.Hkv, self.page, self.d = k.shape
+        self.B, self.max_pages = table.shape
+        self.capacity = self.max_pages * self.page
+        self.dtype, self.device = k.dtype, k.device
+        self.k, self.v, self.table, self.lengths, self.pos, self.seen = k, v, table, lengths, pos, seen
+        strides = []
+        for t in (k, v):
+            _need(t.stride(3) == 1, "the rows of k and v must be contiguous")
+            # a dimension of size one has no stride of its own
+            rs = t.stride(2) if self.page > 1 else self.d
+            hs = t.stride(1) if self.Hkv > 1 else rs * self.page
+            ps = t.stride(0) if self.n_pages > 1 else max(rs * self.page, hs * self.Hkv)
+            strides.append((ps, hs, rs))
+        _need(strides[0] == strides[1], "k and v must have the same strides")
+        _need(min(strides[0]) > 0, "k and v must not be expanded tensors")
+        _need((pos is None) == (seen is None), "pos and seen come together")
+        c = sa_paged_cache(k.data_ptr(), v.data_ptr(),
+                           _dense(table, "table", torch.int32, table.shape, self.device),
+                           _dense(lengths, "lengths", torch.int32, (self.B,), self.device),
+                           None if pos is None else _dense(pos, "pos", torch.int32, self.slots, self.device),
+                           None if seen is None else _dense(seen, "seen", torch.int32, (self.B,), self.device))
+        self._c = c
+        self._shape = sa_paged_shape(self.B, self.Hkv, self.Hkv, self.d, _dtype_code(k), self.n_pages, self.page,
+                                     self.max_pages, 0, *strides[0])
+        self._byref = (ctypes.byref(self._shape), ctypes.byref(c))
+
+    @property
+    def slots(self):
+        """Shape of pos and of the weights: [B, Hkv, slots of a sequence]."""
+        return self.B, self.Hkv, self.capacity
+
+    def _for_heads(self, Hq):
+        """The C shape with Hq query heads."""
+        s = self._shape
+        if s.Hq != Hq:
+            s = sa_paged_shape.from_buffer_copy(s)
+            s.Hq = Hq
+        return s
+
+
+class _On:
+    """The device and stream of a call: the tensors' device, and the given
+    stream or that device's current one, made current while the call runs, so
+    that what it allocates belongs to the stream that uses it."""
+
+    __slots__ = ("stream", "guard")
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if stream is not None:
+            _need(stream.device == device, "the stream is on another device than the tensors")
+            self.guard = torch.cuda.stream(stream)
+            self.stream = stream
+        else:
+            self.stream = torch.cuda.current_stream(device)
+            if torch.cuda.current_device() != device.index:
+                self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+        return False
+
+
+_PAGED_WS = {}
+
+
+def _paged_workspace(shape, op, arg, device, stream):
+    """Scratch of a paged call with its tickets zeroed, kept per (device, stream,
+    op, size, tickets): calls on one stream follow one another, calls on two
+    never share it.  A call that is being captured gets its own, whose tickets
+    the graph zeroes at each replay, so that graphs replayed side by side do not
+    share it either."""
+    n = _lib().sa_paged_workspace_size(ctypes.byref(shape), op, arg)
+    if n == 0:
+        raise SAError(SA_ERR_INVALID_ARG, "sa_paged_workspace_size")
+    # two shapes of one size can have their records where the other has tickets
+    tickets = 4 * shape.B * shape.Hkv * -(-shape.Hq // (8 * shape.Hkv)) if op == OP_PAGED_DECODE else 0
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (device.index, stream, op, n, tickets)
+    ws = None if capturing else _PAGED_WS.get(key)
+    if ws is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if tickets:
+            ws[:tickets].zero_()
+        if not capturing:
+            _PAGED_WS[key] = ws
+    return ws
+
+
+def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
+    """Writes the sequences' newest tokens into their slots (see
+    sa_paged_append).  k_new, v_new [N, Hkv, d] in the cache's type, rows
+    contiguous, same strides (slices of one projection's output will do); start
+    [B + 1] int32: where each sequence's tokens begin in them (None: one token
+    each).  cache.lengths (and cache.seen) already count them.  cache.pos and
+    weight [B, Hkv, capacity] f32, where given, are set for the new slots."""
+    _need(k_new.dim() == 3 and k_new.shape[1:] == (cache.Hkv, cache.d) and k_new.shape == v_new.shape and
+          k_new.dtype == v_new.dtype == cache.dtype and k_new.device == v_new.device == cache.device,
+          "k_new and v_new must be [N, Hkv, d] in the cache's type, on its device")
+    N, ts, hs = k_new.shape[0], k_new.stride(0), k_new.stride(1)
+    if cache.Hkv == 1:
+        hs = cache.d
+    if N == 1:
+        ts = hs * cache.Hkv
+    _need(N == 0 or (k_new.stride(2) == 1 and v_new.stride(2) == 1 and
+                     (N == 1 or (v_new.stride(0) == ts and ts > 0)) and
+                     (cache.Hkv == 1 or (v_new.stride(1) == hs and hs > 0))),
+          "k_new and v_new must have contiguous rows and the same strides")
+    ps = None if start is None else _dense(start, "start", torch.int32, (cache.B + 1,), cache.device)
+    pw = None if weight is None else _dense(weight, "weight", torch.float32, cache.slots, cache.device)
+    with _On(cache.device, stream) as s:
+        _check(_lib().sa_paged_append(*cache._byref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, ps, N, pw, s),
+               "sa_paged_append")
+
+
+def paged_decode(q, cache, scale=0.0, softcap=0.0, sink=0, local=0, slopes=None, weight=None, weight_out=None,
+                 out=None, lse=None, stream=None):
+    """Attention of one query per sequence over its slots (see sa_paged_decode):
+    q [B, Hq, d] in the cache's type (the heads of a sequence dense, any stride
+    between sequences); softcap: logits capped by a tanh; sink, local: with local
+    > 0 only the first `sink` and the last `local` positions are seen; slopes
+    [Hq] f32: times the distance, subtracted from the logits; weight_out [B, Hkv,
+    capacity] f32: weight (None: 0; may be weight_out itself) plus this step's
+    attention weights summed over each KV head's query heads.  Returns (out
+    [B, Hq, d], lse [B, Hq]), fp32."""
+    _need(q.dim() == 3 and q.shape[0] == cache.B and q.shape[2] == cache.d and q.dtype == cache.dtype and
+          q.device == cache.device, "q must be [B, Hq, d] in the cache's type, on its device")
+    B, Hq, d = q.shape
+    _need(Hq > 0 and Hq % cache.Hkv == 0, "the query heads must be a multiple of the KV heads")
+    qs = q.stride(0) if B > 1 else Hq * d
+    _need(q.stride(2) == 1 and (Hq == 1 or q.stride(1) == d) and qs > 0,
+          "the heads of a sequence's query must be dense")
+    dev = cache.device
+    f32 = torch.float32
+    shape = cache._for_heads(Hq)
+    _need(weight is None or weight_out is not None, "weight needs weight_out")
+    p = sa_paged_params(float(scale), float(softcap), int(sink), int(local),
+                        None if slopes is None else _dense(slopes, "slopes", f32, (Hq,), dev),
+                        None if weight is None else _dense(weight, "weight", f32, cache.slots, dev),
+                        None if weight_out is None else _dense(weight_out, "weight_out", f32, cache.slots, dev), qs)
+    with _On(dev, stream) as s:
+        out = torch.empty(B, Hq, d, dtype=f32, device=dev) if out is None else out
+        lse = torch.empty(B, Hq, dtype=f32, device=dev) if lse is None else lse
+        po, pl = _dense(out, "out", f32, (B, Hq, d), dev), _dense(lse, "lse", f32, (B, Hq), dev)
+        ws = _paged_workspace(shape, OP_PAGED_DECODE, int(weight_out is not None), dev, s)
+        _check(_lib().sa_paged_decode(ctypes.byref(shape), cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl,
+                                      ws.data_ptr(), ws.numel(), s), "sa_paged_decode")
+    return out, lse
+
+
+def paged_evict(cache, weight, budget, sink=0, local=0, lengths_out=None, weight_out=None, pos_out=None, stream=None):
+    """Thins every sequence out to `budget` tokens per KV head, keeping the first
+    `sink` and the last `local` positions and then the largest accumulated
+    weights (see sa_paged_evict).  Key and value rows move in place; returns
+    (lengths, weight, pos), new arrays that the cache goes on with:
+
+        lengths, weight, pos = paged_evict(cache, weight, budget, sink, local)
+        cache = PagedCache(cache.k, cache.v, cache.table, lengths, pos, seen)
+
+    where seen counts the tokens each sequence ever had (before the first
+    eviction: the old lengths).  The pages past the new lengths are free."""
+    dev = cache.device
+    pw = _dense(weight, "weight", torch.float32, cache.slots, dev)
+    shape = cache._shape
+    with _On(dev, stream) as s:
+        i32 = dict(dtype=torch.int32, device=dev)
+        lengths_out = torch.empty(cache.B, **i32) if lengths_out is None else lengths_out
+        weight_out = torch.zeros(cache.slots, dtype=torch.float32, device=dev) if weight_out is None else weight_out
+        pos_out = torch.zeros(cache.slots, **i32) if pos_out is None else pos_out
+        po = (_dense(lengths_out, "lengths_out", torch.int32, (cache.B,), dev),
+              _dense(weight_out, "weight_out", torch.float32, cache.slots, dev),
+              _dense(pos_out, "pos_out", torch.int32, cache.slots, dev))
+        _need(0 < int(budget) < 2 ** 31, "budget must be a positive int32")
+        ws = _paged_workspace(shape, OP_PAGED_EVICT, int(budget), dev, s)
+        _check(_lib().sa_paged_evict(*cache._byref, pw, int(budget), int(sink), int(local), *po, ws.data_ptr(),
+                                     ws.numel(), s), "sa_paged_evict")
+    return lengths_out, weight_out, pos_out
 
 
 def wait_timeouts():

@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsa_b200.so")
 SOURCES = ["sa_api.cu", "sa_prefill.cu", "sa_select.cu", "sa_decode.cu", "sa_clt.cu", "sa_select_var.cu", "sa_multi.cu", "sa_qgc.cu", "sa_noalloc.cu",
-           "sa_append.cu"]
+           "sa_append.cu", "sa_paged_api.cu", "sa_paged_append.cu", "sa_paged_decode.cu", "sa_paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(ROOT, "include")]

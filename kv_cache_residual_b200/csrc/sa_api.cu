@@ -1,22 +1,12 @@
 // C ABI of libsa_b200.so (declared in include/sa_decode.h): argument checks,
 // workspace sizing, and dispatch to the kernel launchers.  Every check runs
 // before anything is enqueued, so a rejected call leaves the stream untouched.
-#include <math.h>
-#include <nvtx3/nvToolsExt.h>
-
+#include "sa_check.h"
 #include "sa_internal.h"
 
 using namespace sa;
 
 namespace {
-
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-};
-
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 sa_status check_shape(const sa_shape* s, Dims* d) {
     if (s == nullptr) return SA_ERR_INVALID_ARG;
@@ -69,8 +59,6 @@ bool check_stats(const sa_stats* st, bool need_all) {
     }
     return true;
 }
-
-float resolve_scale(float scale, int d) { return scale > 0.f ? scale : (float)(1.0 / sqrt((double)d)); }
 
 }  // namespace
 

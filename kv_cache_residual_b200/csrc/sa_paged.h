@@ -1,0 +1,121 @@
+// Host-side plans and launchers of the paged cache's operators, and the
+// arguments their kernels share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "sa_internal.h"
+
+namespace sa {
+
+constexpr int kPgTile = 64;            // slots per tile: the unit of the split over a cache's length
+constexpr int kPgHeads = 8;            // query heads of one unit; wider groups are several units per KV head
+constexpr int kPgSlots = 148 * 2;      // CTAs of the decode: two per SM
+
+struct PagedDims {
+    int B, Hq, Hkv, G, d;
+    int bf16;
+    int n_pages, page, shift, max_pages;   // shift: log2(page), or -1
+    int cap, ldw;                          // slots per sequence, row length of pos and of the weights
+    int nhb;                               // units per KV head
+    long long ps, hs, rs;                  // page, head and row strides (elements)
+    int U() const { return B * Hkv; }
+    int esz() const { return bf16 ? 2 : 4; }
+};
+
+// What the kernels of the three operators read of a cache.
+struct PagedView {
+    const void* k;
+    const void* v;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* pos;
+    const int32_t* seen;
+    int B, Hq, Hkv, G, nhb;
+    int n_pages, page, shift, max_pages, cap, ldw;
+    long long ps, hs, rs;
+};
+
+inline PagedView paged_view(const PagedDims& d, const sa_paged_cache& c) {
+    return PagedView{c.k, c.v, c.table, c.lengths, c.pos, c.seen, d.B, d.Hq, d.Hkv, d.G, d.nhb,
+                     d.n_pages, d.page, d.shift, d.max_pages, d.cap, d.ldw, d.ps, d.hs, d.rs};
+}
+
+// Decode: the tiles of all units, in unit order, are split evenly over at
+// most kPgSlots CTAs (on the device, from the lengths there), so a CTA ends
+// at most two units it does not own alone: one record for the unit it
+// continues, one for the unit it begins.
+struct PagedDecodePlan {
+    int grid;
+    int rec;                               // floats per record: m[8], l[8], acc[8][d]
+    size_t off_cnt, off_rec, off_lse, off_x, bytes;
+};
+
+inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
+    PagedDecodePlan p;
+    const long long tiles = (long long)d.U() * d.nhb * ((d.cap + kPgTile - 1) / kPgTile);
+    p.grid = (int)(tiles < kPgSlots ? tiles : kPgSlots);
+    p.rec = kPgHeads * (2 + d.d);
+    size_t off = 0;
+    p.off_cnt = off; off = align256(off + sizeof(unsigned) * (size_t)d.U() * d.nhb);
+    p.off_rec = off; off = align256(off + sizeof(float) * 2 * (size_t)p.grid * p.rec);
+    // with weights: log2 of every row's mass, and the logits (log2) of every
+    // slot, heads of a group side by side
+    p.off_lse = off; if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq);
+    p.off_x = off;   if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq * d.cap);
+    p.bytes = off;
+    return p;
+}
+
+struct PagedDecodeArgs {
+    PagedView c;
+    const void* q;
+    long long q_stride;
+    const float* slopes;
+    const float* weight;
+    float* weight_out;
+    float* out;
+    float* lse;
+    float scale, softcap;
+    int sink, local;
+    char* ws;
+};
+cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, const PagedDecodeArgs& a,
+                                cudaStream_t s);
+
+struct PagedAppendArgs {
+    PagedView c;
+    const void* k_new;
+    const void* v_new;
+    long long token_stride, head_stride;
+    const int32_t* start;
+    int n_new;
+    int32_t* pos;
+    float* weight;
+};
+cudaError_t launch_paged_append(const PagedDims& d, const PagedAppendArgs& a, cudaStream_t s);
+
+// Eviction: a cluster of CTAs per (sequence, KV head); scratch: its freed
+// slots and the late kept slots that move into them.
+struct PagedEvictPlan {
+    int cluster, slice_max;                // CTAs per unit, most slots of one
+    int moves;                             // most moves of a unit
+    size_t off_list, bytes;
+};
+
+PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget);
+
+struct PagedEvictArgs {
+    PagedView c;
+    const float* weight;
+    int budget, sink, local;
+    int32_t* lengths_out;
+    float* weight_out;
+    int32_t* pos_out;
+    char* ws;
+};
+cudaError_t launch_paged_evict(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s);
+
+}  // namespace sa

@@ -1,0 +1,119 @@
+// Device code shared by the paged decode kernels: logits, records of partial
+// units and their join.
+#pragma once
+
+#include "sa_cta.cuh"
+#include "sa_paged.cuh"
+
+namespace sa {
+
+struct PgDecodeIo {
+    PagedView c;
+    const void* q;
+    long long q_stride;
+    const float* slopes;
+    float* out;
+    float* lse;
+    float* lse2;             // with weights: log2 of the rows' masses
+    float* x;                // with weights: logits (log2) [B, Hkv, cap, G], or null
+    float* rec;              // two records per CTA
+    unsigned* cnt;           // completion tickets, one per unit
+    float scale, qscale;     // softmax scale, and times log2(e)
+    float softcap, cap_in, cap_out;    // c, scale / c, c log2(e)
+    int sink, local, min_tiles;
+};
+
+// logit in log2 units: the dot product scaled, capped (tanhf: 2 ulp, so that
+// the capped logit is as exact as the dot product), and biased by distance
+__device__ __forceinline__ float pg_logit(const PgDecodeIo& io, float dot, float slope2, float dist) {
+    const float x = io.softcap > 0.f ? io.cap_out * tanhf(dot * io.cap_in) : dot * io.qscale;
+    return fmaf(-slope2, dist, x);
+}
+
+// Whether the token of a listed slot is visible, its row offset (-1: not) and
+// its distance from the newest position.
+__device__ __forceinline__ long long pg_see(const PgDecodeIo& io, const int32_t* trow, int b, int g, int slot,
+                                            int newest, float& dist) {
+    long long away = (long long)newest - slot;
+    if (io.c.pos != nullptr) {
+        const int p = __ldg(io.c.pos + ((size_t)b * io.c.Hkv + g) * io.c.ldw + slot);
+        away = (long long)newest - p;
+        if (io.local > 0 && !(p < io.sink || away < io.local)) {
+            dist = 0.f;
+            return -1;
+        }
+    }
+    dist = (float)away;
+    return pg_row(io.c, trow, g, slot);
+}
+
+// Records of a unit, in split order: its first CTA's second record, then the
+// first records of the CTAs after it.
+__device__ __forceinline__ float* pg_rec(float* rec, int floats, int cta, bool begins) {
+    return rec + (size_t)(2 * cta + (begins ? 1 : 0)) * floats;
+}
+
+// one row's outputs: accumulator A of dim e, mass L relative to 2^M
+template <int D>
+__device__ __forceinline__ void pg_write(const PgDecodeIo& io, size_t qh, int e, float A, float M, float L) {
+    io.out[qh * D + e] = L == 0.f ? 0.f : A / L;
+    if (e == 0) {
+        const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
+        if (io.lse != nullptr) io.lse[qh] = l2 * kLn2;
+        if (io.x != nullptr) io.lse2[qh] = l2;
+    }
+}
+
+// The unit's last CTA joins its n records (fixed order) and writes the rows of
+// its gh heads.  f: shared scratch of 8 n + 16 floats.
+template <int D, int NT>
+__device__ void pg_join(const PgDecodeIo& io, int floats, int first, int n, size_t qh0, int gh, float* f) {
+    float* sM = f;
+    float* sL = f + kPgHeads;
+    float* w = f + 2 * kPgHeads;               // [head][record] weights 2^(m - M)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto rec = [&](int s) -> const float* { return pg_rec(io.rec, floats, first + s, s == 0); };
+    for (int h = warp; h < gh; h += NT / 32) {
+        float M = -INFINITY;
+        for (int s = lane; s < n; s += 32) {
+            const float m = __ldcg(rec(s) + h);
+            w[h * n + s] = m;
+            M = (m > M || m != m) ? m : M;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, M, o);
+            M = (y > M || y != y) ? y : M;
+        }
+        float L = 0.f;
+        for (int s = lane; s < n; s += 32) {
+            const float m = w[h * n + s];
+            const float x = m == -INFINITY ? 0.f : ex2(m - M);
+            w[h * n + s] = x;
+            L = fmaf(__ldcg(rec(s) + kPgHeads + h), x, L);
+        }
+        L = group_sum<32>(L);
+        if (lane == 0) { sM[h] = M; sL[h] = L; }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < gh * (D / 4); x += NT) {
+        const int h = x / (D / 4), e = (x % (D / 4)) * 4;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int s = 0; s < n; ++s) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(rec(s) + 2 * kPgHeads + h * D + e));
+            const float y = w[h * n + s];
+            A.x = fmaf(a.x, y, A.x);
+            A.y = fmaf(a.y, y, A.y);
+            A.z = fmaf(a.z, y, A.z);
+            A.w = fmaf(a.w, y, A.w);
+        }
+        const float M = sM[h], L = sL[h];
+        pg_write<D>(io, qh0 + h, e, A.x, M, L);
+        pg_write<D>(io, qh0 + h, e + 1, A.y, M, L);
+        pg_write<D>(io, qh0 + h, e + 2, A.z, M, L);
+        pg_write<D>(io, qh0 + h, e + 3, A.w, M, L);
+    }
+}
+
+}  // namespace sa

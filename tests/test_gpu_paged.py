@@ -1,0 +1,668 @@
+"""GPU parity of the paged cache's operators (sa_paged_append, sa_paged_decode,
+sa_paged_evict) against the fp64 oracle: cache forms, masks, sizes, strides and
+streams, and a run of the three together.
+
+Append and eviction move bits: they are compared exactly.  The decode's bound,
+with u = 2^-24 (half a step of fp32):
+  logit    d products summed in blocks of 16, each block off by at most 4 last
+           places (8 u) whether by fused adds or by a matrix instruction, the
+           blocks' sum likewise: 8 u (d/16 + 4) scale sum_e |q_e k_e|; then scaling,
+           cap (tanhf: 2 places) and bias: 8 u of each term
+  weight   relative: the logit's error, once for the weight and once for the sum;
+           2^x off by 2^-22 at each of at most 24 rescalings and joins
+  sum      one lane adds at most n/8 + 64 terms one after another: that many u
+The capped, biased logit is bounded term by term, and every term relative to
+sum p |v|, so no entry's own cancellation enters."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_residual_b200 as sa
+from oracle import paged as opaged
+from parity_util import f64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _dev():
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+class Case:
+    """A paged cache on the GPU.  Everything in the pools that no live slot
+    holds is NaN."""
+
+    def __init__(self, lens, Hkv=2, G=4, d=128, page=16, dtype=BF, layout="heads", tracked=False, cols=None, seed=0,
+                 scale_k=1.0):
+        r = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        dev = _dev()
+        self.B, self.Hkv, self.G, self.d, self.page, self.dtype = len(lens), Hkv, G, d, page, dtype
+        self.Hq = Hkv * G
+        self.lens = list(lens)
+        self.cols = max(1, -(-max(lens) // page)) if cols is None else cols
+        self.cap = self.cols * page
+        self.n_pages = self.B * self.cols + 2
+        nan = dict(fill_value=float("nan"), dtype=dtype, device=dev)
+        n, H, p = self.n_pages, Hkv, page
+        if layout == "heads":                      # [n_pages, Hkv, page, d]
+            k, v = torch.full((n, H, p, d), **nan), torch.full((n, H, p, d), **nan)
+        elif layout == "rows":                     # [n_pages, page, Hkv, d]
+            k, v = (torch.full((n, p, H, d), **nan).transpose(1, 2) for _ in range(2))
+        elif layout == "both":                     # [n_pages, 2, Hkv, page, d]
+            kv = torch.full((n, 2, H, p, d), **nan)
+            k, v = kv[:, 0], kv[:, 1]
+        else:                                      # rows padded by 16 bytes, pages and heads by more
+            pad = 16 // torch.tensor([], dtype=dtype).element_size()
+            k, v = (torch.full((n, H + 1, p + 1, d + pad), **nan)[:, :H, :p, :d] for _ in range(2))
+        self.k, self.v = k, v
+        self.table_h = r.permutation(n)[:self.B * self.cols].reshape(self.B, self.cols).astype(np.int32)
+        self.table = torch.from_numpy(self.table_h).to(dev)
+        self.lengths = torch.tensor(lens, dtype=I32, device=dev)
+        for b, L in enumerate(lens):
+            pg, row, _ = opaged.slot_pages(self.table_h[b], L, page, n)
+            pg, row = torch.from_numpy(pg).long().to(dev), torch.from_numpy(row).to(dev)
+            for t, f in ((k, scale_k), (v, 1.0)):
+                x = torch.randn(L, H, d, generator=g, device=dev) * f
+                t[pg, :, row] = x.to(dtype)
+        self.q = torch.randn(self.B, self.Hq, d, generator=g, device=dev).to(dtype)
+        self.pos = self.seen = None
+        if tracked:
+            self.seen_h = [L + L // 2 + 1 for L in lens]
+            pos = np.full((self.B, Hkv, self.cap), -7, dtype=np.int32)
+            for b, L in enumerate(lens):
+                for h in range(Hkv):
+                    pos[b, h, :L] = r.permutation(self.seen_h[b])[:L]
+                    if L:
+                        pos[b, h, r.integers(L)] = self.seen_h[b] - 1
+            self.pos = torch.from_numpy(pos).to(dev)
+            self.seen = torch.tensor(self.seen_h, dtype=I32, device=dev)
+        self.weight = torch.rand(self.B, Hkv, self.cap, generator=g, device=dev)
+
+    def cache(self, **kw):
+        a = dict(k=self.k, v=self.v, table=self.table, lengths=self.lengths, pos=self.pos, seen=self.seen)
+        a.update(kw)
+        return sa.PagedCache(*[a[n] for n in ("k", "v", "table", "lengths", "pos", "seen")])
+
+    def unit(self, b, h):
+        """Rows, positions, newest position and valid slots of a unit, on the host."""
+        L = min(max(int(self.lengths[b]), 0), self.cap)
+        pg, row, ok = opaged.slot_pages(self.table.cpu().numpy()[b], L, self.page, self.n_pages)
+        at = np.where(ok, pg, 0)
+        K, V = f64(self.k[at, h, row]), f64(self.v[at, h, row])
+        pos = np.arange(L) if self.pos is None else self.pos[b, h, :L].cpu().numpy()
+        newest = (L if self.seen is None else int(self.seen[b])) - 1
+        return L, K, V, pos, newest, ok
+
+
+def _check_decode(c, out, lse, weight_out=None, weight=None, before=None, scale=0.0, softcap=0.0, sink=0, local=0,
+                  slopes=None):
+    s = scale if scale > 0 else 1.0 / math.sqrt(c.d)
+    q = f64(c.q)
+    sl = None if slopes is None else f64(slopes)
+    out, lse = f64(out), f64(lse)
+    wo = None if weight_out is None else f64(weight_out)
+    for b in range(c.B):
+        for h in range(c.Hkv):
+            L, K, V, pos, newest, ok = c.unit(b, h)
+            sees = ok & opaged.visible(pos, newest, sink, local)
+            at = slice(h * c.G, (h + 1) * c.G)
+            slu = None if sl is None else sl[at]
+            ro, rl, p = opaged.decode_unit(q[b, at], K, V, pos, newest, sees, s, softcap, slu)
+            w = (b, h)
+            if not sees.any():
+                assert not out[b, at].any() and np.all(lse[b, at] == -np.inf), w
+                dp = np.zeros((c.G, 1))
+            else:
+                Ks, Vs = K[sees], V[sees]
+                mag = s * (np.abs(q[b, at]) @ np.abs(Ks).T)
+                dx = 8 * U * (c.d / 16 + 4) * mag + 8 * U * mag
+                if softcap > 0:
+                    dx = dx + 8 * U * softcap
+                if slu is not None:
+                    dx = dx + 8 * U * slu[:, None] * (newest - pos[sees])
+                    dx = dx + 8 * U * slu[:, None] * np.abs(newest - pos[sees])
+                live = p[:, sees] > 1e-12                  # a weight below that does not show
+                dx = np.where(live, dx, 0.0).max(axis=1)
+                rel = np.expm1(dx) + 24 * 1.25 * 2.0 ** -22 + (L / 8 + 64) * U
+                tol = (2 * rel + 1e-9)[:, None] * (p[:, sees] @ np.abs(Vs)) + 1e-9
+                assert np.all(np.abs(out[b, at] - ro) <= tol), (w, np.max(np.abs(out[b, at] - ro) / tol))
+                tl = rel + 4 * U * np.abs(rl) + dx
+                assert np.all(np.abs(lse[b, at] - rl) <= tl), (w, lse[b, at], rl)
+                dp = (2 * rel + 1e-9)[:, None]
+            if wo is not None:
+                w0 = np.zeros(c.cap) if weight is None else f64(weight[b, h])
+                want = w0[:L] + p.sum(axis=0)
+                tol = (dp * p).sum(axis=0) + 8 * U * (np.abs(w0[:L]) + p.sum(axis=0)) + 1e-12 * c.G
+                assert np.all(np.abs(wo[b, h, :L] - want) <= tol), w
+                assert np.array_equal(wo[b, h, L:], f64(before[b, h, L:])), w
+
+
+def _decode(c, weights=False, cache=None, **kw):
+    args = dict(kw)
+    before = None
+    if weights:
+        before = torch.full((c.B, c.Hkv, c.cap), -3.0, device=_dev())
+        args.update(weight=c.weight, weight_out=before.clone())
+    out, lse = sa.paged_decode(c.q, cache or c.cache(), **args)
+    torch.cuda.synchronize()
+    _check_decode(c, out, lse, args.get("weight_out"), c.weight if weights else None, before, **kw)
+    return out, lse
+
+
+LENS = [[1], [0, 1, 15, 16, 17, 63], [64, 65, 0, 127, 128, 129], [1000, 3], [5003]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 4), (BF, 64, 8), (F32, 128, 2), (F32, 64, 1)])
+def test_decode_lengths(lens, dtype, d, G):
+    c = Case(lens, G=G, d=d, dtype=dtype, seed=1)
+    _decode(c)
+    _decode(c, weights=True)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8, 9, 12, 16, 17, 24])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_decode_groups(G, dtype, d):
+    c = Case([130, 0, 777], Hkv=3, G=G, d=d, dtype=dtype, seed=2)
+    _decode(c, weights=True, softcap=3.0)
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 64, 100, 128])
+@pytest.mark.parametrize("layout", ["heads", "rows", "both", "padded"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_pages_and_strides(page, layout, dtype):
+    c = Case([333, 1, 64, 200], page=page, layout=layout, dtype=dtype, seed=3)
+    _decode(c)
+    _decode(c, sink=5, local=77)
+
+
+@pytest.mark.parametrize("sink,local", [(0, 1), (0, 64), (64, 2000), (3, 100), (200, 1), (5000, 5000), (1, 63)])
+@pytest.mark.parametrize("tracked", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_windows(sink, local, tracked, dtype):
+    c = Case([2500, 64, 0, 1, 300], tracked=tracked, dtype=dtype, seed=4)
+    slopes = torch.exp2(-torch.arange(1, c.Hq + 1, device=_dev(), dtype=F32))
+    _decode(c, sink=sink, local=local)
+    _decode(c, weights=True, sink=sink, local=local, slopes=slopes, softcap=20.0)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 0.5, 30.0])
+@pytest.mark.parametrize("scale", [0.0, 0.7])
+@pytest.mark.parametrize("biased", [False, True])
+def test_decode_scores(softcap, scale, biased):
+    for dtype in (BF, F32):
+        c = Case([900, 31], dtype=dtype, seed=5, tracked=biased)
+        slopes = torch.linspace(0.0, 0.5, c.Hq, device=_dev()) if biased else None
+        _decode(c, weights=True, softcap=softcap, scale=scale, slopes=slopes)
+
+
+def test_decode_rising_scores():
+    """Logits that grow along the cache: the running maximum moves at every row."""
+    for dtype in (BF, F32):
+        c = Case([1500], dtype=dtype, seed=6)
+        pg, row, _ = opaged.slot_pages(c.table_h[0], 1500, c.page, c.n_pages)
+        ramp = torch.linspace(0, 3, 1500, device=_dev())[:, None, None]
+        c.k[pg, :, row] = (c.q[0].float().view(c.Hkv, c.G, c.d).mean(1)[None] * ramp).to(dtype)
+        _decode(c, weights=True)
+
+
+@pytest.mark.parametrize("tracked", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_masked_slots_are_not_read(tracked, dtype):
+    """Infinities and NaN in the keys and values of slots a query does not see."""
+    c = Case([700, 90], tracked=tracked, dtype=dtype, seed=7)
+    sink, local = 10, 120
+    for b in range(c.B):
+        for h in range(c.Hkv):
+            L, K, V, pos, newest, ok = c.unit(b, h)
+            out = np.nonzero(~opaged.visible(pos, newest, sink, local))[0]
+            pg, row, _ = opaged.slot_pages(c.table_h[b], L, c.page, c.n_pages)
+            for i, bad in enumerate((float("nan"), float("inf"), float("-inf"))):
+                at = out[i::3]
+                c.k[pg[at], h, row[at]] = bad
+                c.v[pg[at], h, row[at]] = bad
+    _decode(c, weights=True, sink=sink, local=local)
+
+
+def test_decode_sees_nothing():
+    c = Case([40, 5, 0], tracked=True, seed=8)
+    c.seen += 10000                                     # every position lies before the window
+    c.k.fill_(float("nan"))
+    c.v.fill_(float("nan"))
+    out, lse = _decode(c, weights=True, local=50)
+    assert not out.any() and torch.all(lse == -math.inf)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_bad_pages_are_masked(dtype):
+    c = Case([200, 64, 33], dtype=dtype, seed=9)
+    c.table[0, 2], c.table[0, 12], c.table[2, 0] = -1, c.n_pages, 2 ** 31 - 1
+    c.table[1, :] = -(2 ** 31)
+    out, lse = _decode(c, weights=True)
+    assert not out[1].any()
+
+
+def test_decode_lengths_are_clamped():
+    c = Case([64, 50], cols=4, seed=10)
+    c.lengths.copy_(torch.tensor([1 << 30, -5]))
+    _decode(c, weights=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_infinite_logits(dtype):
+    """A key at -inf along a head's query has weight 0 there; NaN in a seen row
+    stays within its unit."""
+    c = Case([70, 70], dtype=dtype, seed=11)
+    base, _ = sa.paged_decode(c.q, c.cache())
+    pg, row, _ = opaged.slot_pages(c.table_h[0], 70, c.page, c.n_pages)
+    c.q[0, 0] = 0.0
+    c.q[0, 0, 0] = 1.0
+    c.q[0, 1:c.G, 0] = 1.0
+    for s in (0, 69):
+        c.k[pg[s], 0, row[s]] = 0.0
+        c.k[pg[s], 0, row[s], 0] = float("-inf")
+    out, lse = sa.paged_decode(c.q, c.cache())
+    L, K, V, pos, newest, _ = c.unit(0, 0)
+    sees = np.ones(70, dtype=bool)
+    sees[[0, 69]] = False
+    ro, rl, _ = opaged.decode_unit(f64(c.q[0, :c.G]), K, V, pos, newest, sees, 1 / math.sqrt(c.d))
+    assert np.allclose(f64(out[0, 0]), ro[0], rtol=0, atol=1e-4) and abs(float(lse[0, 0]) - rl[0]) < 1e-4
+    c.k[pg[3], 1, row[3], 5] = float("nan")
+    out, lse = sa.paged_decode(c.q, c.cache())
+    assert torch.isnan(out[0, c.G:2 * c.G]).all() and torch.isnan(lse[0, c.G:2 * c.G]).all()
+    assert torch.isfinite(out[0, 0]).all() and torch.equal(out[1], base[1])
+
+
+def test_decode_query_strides_and_outputs():
+    c = Case([100, 20, 7], seed=12)
+    fused = torch.randn(c.B, c.Hq + 2 * c.Hkv, c.d, device=_dev()).to(BF)
+    c.q = fused[:, :c.Hq]
+    out, lse = torch.empty(c.B, c.Hq, c.d, device=_dev()), torch.empty(c.B, c.Hq, device=_dev())
+    o, l = sa.paged_decode(c.q, c.cache(), out=out, lse=lse)
+    assert o is out and l is lse
+    _check_decode(c, out, lse)
+
+
+def test_decode_weights_in_place_and_from_nothing():
+    c = Case([300, 0, 17], seed=13)
+    none = torch.full((c.B, c.Hkv, c.cap), 5.0, device=_dev())
+    before = none.clone()
+    out, lse = sa.paged_decode(c.q, c.cache(), weight_out=none)
+    _check_decode(c, out, lse, none, None, before)
+    acc, start = c.weight.clone(), c.weight.clone()
+    sa.paged_decode(c.q, c.cache(), weight=acc, weight_out=acc)
+    _check_decode(c, out, lse, acc, start, start)
+
+
+def test_decode_many_sequences():
+    """More sequences than threads of a CTA, most of them short or empty."""
+    r = np.random.default_rng(14)
+    c = Case([int(x) for x in r.integers(0, 40, 600)], Hkv=1, G=4, d=64, cols=3, seed=14)
+    _decode(c)
+    c = Case([0] * 300 + [900] + [0] * 50, Hkv=2, d=64, cols=57, seed=15)
+    _decode(c, weights=True)
+
+
+def test_decode_repeats_bit_for_bit():
+    c = Case([9000, 100, 4000], seed=16)
+    cache = c.cache()
+    a = sa.paged_decode(c.q, cache)
+    for _ in range(5):
+        b = sa.paged_decode(c.q, cache)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_workspaces_of_one_size():
+    """Shapes whose workspaces have one size but not the same tickets."""
+    for B, Hkv in ((1, 2), (2, 4), (4, 8), (1, 16), (3, 2)):
+        c = Case([5000] + [600] * (B - 1), Hkv=Hkv, d=64, seed=17)
+        _decode(c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_past_32_bits(dtype):
+    """Pages whose rows start beyond 2^31 elements, in a token-major pool."""
+    dev = _dev()
+    H, d, page = 8, 128, 64
+    n = 2 ** 31 // (H * d * page) + 40
+    k = torch.empty(n, page, H, d, dtype=dtype, device=dev).transpose(1, 2)
+    v = torch.empty(n, page, H, d, dtype=dtype, device=dev).transpose(1, 2)
+    c = Case([500], Hkv=H, G=2, page=page, dtype=dtype, seed=18)
+    c.table_h = c.table_h * 0 + np.arange(n - c.cols, n, dtype=np.int32)[None, ::-1]
+    for i in range(c.cols):
+        k[int(c.table_h[0, i])] = c.k[int(c.table[0, i])]
+        v[int(c.table_h[0, i])] = c.v[int(c.table[0, i])]
+    c.k, c.v, c.n_pages = k, v, n
+    c.table.copy_(torch.from_numpy(c.table_h.copy()))
+    _decode(c)
+    new = torch.randn(1, H, d, device=dev).to(dtype)
+    sa.paged_append(c.cache(), new, -new)
+    assert torch.equal(k[int(c.table_h[0, 499 // page]), :, 499 % page], new[0])
+    _decode(c)
+    _evict(c, 200, 4, 30)
+
+
+# ---- append ------------------------------------------------------------------
+
+def _pools(c):
+    return f64(c.k).copy(), f64(c.v).copy()
+
+
+@pytest.mark.parametrize("page", [1, 16, 24])
+@pytest.mark.parametrize("layout", ["heads", "rows", "both", "padded"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("one", [True, False])
+def test_append(page, layout, dtype, d, one):
+    c = Case([40, 1, 77, 9], page=page, layout=layout, dtype=dtype, d=d, tracked=True, seed=20)
+    n = [1] * 4 if one else [7, 0, 77, 2]
+    start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    N = int(start[-1])
+    dev = _dev()
+    fused = torch.randn(N, 3 * c.Hkv, d, device=dev).to(dtype)
+    kn, vn = fused[:, :c.Hkv], fused[:, c.Hkv:2 * c.Hkv]
+    K, V = _pools(c)
+    pos, w = c.pos.cpu().numpy().copy(), f64(c.weight).copy()
+    for b in range(4):
+        for j in range(n[b]):
+            s = c.lens[b] - n[b] + j
+            pg, row = c.table_h[b, s // page], s % page
+            K[pg, :, row], V[pg, :, row] = f64(kn[start[b] + j]), f64(vn[start[b] + j])
+            pos[b, :, s], w[b, :, s] = c.seen_h[b] - n[b] + j, 0.0
+    sa.paged_append(c.cache(), kn, vn, start=None if one else torch.from_numpy(start).to(dev), weight=c.weight)
+    torch.cuda.synchronize()
+    for got, want in ((f64(c.k), K), (f64(c.v), V), (f64(c.weight), w)):
+        assert np.array_equal(got, want, equal_nan=True)
+    assert np.array_equal(c.pos.cpu().numpy(), pos)
+
+
+def test_append_skips_what_has_no_place():
+    """Tokens outside every sequence, more of them than the sequence is long,
+    pages that are not the pool's, lengths past the capacity."""
+    dev = _dev()
+    c = Case([20, 3, 30, 64], cols=4, seed=21)
+    c.lengths[3] = 1000                                             # clamped to 64
+    c.table[2, 1], c.table[2, 0] = -1, c.n_pages
+    new = torch.randn(30, c.Hkv, c.d, device=dev).to(BF)
+    K, V = _pools(c)
+    start = torch.tensor([2, 6, 12, 25, 28], dtype=I32, device=dev)     # 4, 6, 13 and 3 tokens
+    for b, toks, first in ((0, range(2, 6), 16), (1, range(9, 12), 0), (3, range(25, 28), 61)):
+        for j, t in enumerate(toks):
+            pg, row = c.table_h[b, (first + j) // 16], (first + j) % 16
+            K[pg, :, row], V[pg, :, row] = f64(new[t]), f64(-new[t])
+    sa.paged_append(c.cache(), new, -new, start=start)
+    assert np.array_equal(f64(c.k), K, equal_nan=True) and np.array_equal(f64(c.v), V, equal_nan=True)
+    sa.paged_append(c.cache(), new[:0], new[:0], start=start * 0)
+    assert np.array_equal(f64(c.k), K, equal_nan=True)
+
+
+def test_append_many_tokens():
+    c = Case([3000, 5000, 1], Hkv=4, layout="rows", page=64, seed=22)
+    dev = _dev()
+    new = torch.randn(8001, 4, c.d, device=dev).to(BF)
+    start = torch.tensor([0, 3000, 8000, 8001], dtype=I32, device=dev)
+    sa.paged_append(c.cache(), new, -new, start=start)
+    for b in range(3):
+        pg, row, _ = opaged.slot_pages(c.table_h[b], c.lens[b], 64, c.n_pages)
+        assert torch.equal(c.k[pg, :, row], new[int(start[b]):int(start[b + 1])])
+        assert torch.equal(c.v[pg, :, row], -new[int(start[b]):int(start[b + 1])])
+
+
+# ---- eviction ----------------------------------------------------------------
+
+def _evict(c, budget, sink, local, **kw):
+    """Runs the eviction and compares everything it writes, and all it must not."""
+    dev = _dev()
+    K0, V0 = c.k.clone(), c.v.clone()
+    units = [(b, h, c.unit(b, h)) for b in range(c.B) for h in range(c.Hkv)]
+    wo = torch.full((c.B, c.Hkv, c.cap), -3.0, device=dev)
+    po = torch.full((c.B, c.Hkv, c.cap), -9, dtype=I32, device=dev)
+    lo, w2, p2 = sa.paged_evict(c.cache(), c.weight, budget, sink, local, weight_out=wo, pos_out=po, **kw)
+    assert w2 is wo and p2 is po
+    torch.cuda.synchronize()
+    W, P = wo.cpu().numpy(), po.cpu().numpy()
+    wt = c.weight.cpu().numpy()
+    for b, h, (L, K, V, pos, newest, ok) in units:
+        src = opaged.evict_unit(wt[b, h, :L], pos, newest, budget, sink, local)
+        n = min(L, budget)
+        assert int(lo[b]) == n and len(src) == n
+        assert np.array_equal(W[b, h, :n], wt[b, h, src], equal_nan=True), (b, h)
+        assert np.array_equal(P[b, h, :n], pos[src]), (b, h)
+        assert np.all(W[b, h, n:] == -3.0) and np.all(P[b, h, n:] == -9)
+        tb = c.table.cpu().numpy()[b]
+        moved = np.nonzero(src != np.arange(n))[0]
+        frm = src[moved]
+        fine = ok[moved] & ok[frm]
+        moved, frm = moved[fine], frm[fine]
+        for now, old in ((c.k, K0), (c.v, V0)):
+            x = old[tb[frm // c.page], h, frm % c.page]
+            old[tb[moved // c.page], h, moved % c.page] = x
+    bits = torch.int16 if c.dtype == BF else torch.int32
+    assert torch.equal(c.k.view(bits), K0.view(bits)) and torch.equal(c.v.view(bits), V0.view(bits))
+    return lo, wo, po
+
+
+@pytest.mark.parametrize("budget,sink,local", [(1, 0, 0), (1, 0, 1), (16, 4, 4), (100, 0, 100), (100, 30, 10), (299, 4, 32),
+                                               (300, 4, 32), (5000, 64, 128)])
+@pytest.mark.parametrize("tracked", [False, True])
+@pytest.mark.parametrize("dtype,d,layout", [(BF, 128, "heads"), (F32, 64, "rows"), (F32, 128, "both"), (BF, 64, "padded")])
+def test_evict(budget, sink, local, tracked, dtype, d, layout):
+    c = Case([300, 0, 1, 299, 17, 2000], d=d, dtype=dtype, layout=layout, tracked=tracked, page=24, seed=30)
+    _evict(c, budget, sink, local)
+
+
+def test_evict_odd_weights():
+    """Ties, both zeros, infinities, NaN, negative and subnormal weights."""
+    inf, nan = math.inf, math.nan
+    pool = torch.tensor([0.0, -0.0, 1.0, 1.0, 1.0, inf, -inf, nan, -1.0, 1e-40, 2e-40, 3.4e38, -nan], device=_dev())
+    for budget in (5, 64, 150, 333):
+        c = Case([400, 334, 20], seed=31)
+        c.weight = pool[torch.randint(0, 13, c.weight.shape, device=_dev(),
+                                      generator=torch.Generator(device="cuda").manual_seed(budget))]
+        _evict(c, budget, 2, 3)
+        c.weight = torch.ones_like(c.weight)
+        _evict(c, budget, 0, 0)
+        c.weight = torch.full_like(c.weight, nan)
+        _evict(c, budget, 1, 0)
+
+
+def test_evict_bad_pages_and_lengths():
+    c = Case([200, 100, 64], cols=13, seed=32)
+    c.table[0, 0], c.table[0, 10], c.table[1, 3] = -1, c.n_pages, 2 ** 31 - 1
+    c.lengths[2] = 1 << 30
+    _evict(c, 60, 4, 8)
+
+
+def test_evict_long_units():
+    """Slices too long for the keys in shared memory, one unit and several."""
+    c = Case([420001], Hkv=1, G=1, d=64, page=64, seed=33)
+    _evict(c, 100000, 64, 128)
+    c = Case([60000, 70003], Hkv=2, G=1, d=64, page=16, layout="rows", tracked=True, seed=34)
+    c.weight = (c.weight * 50).floor()                  # many ties
+    _evict(c, 20000, 64, 128)
+
+
+def test_evict_many_units():
+    r = np.random.default_rng(35)
+    c = Case([int(x) for x in r.integers(0, 90, 200)], Hkv=4, G=1, d=64, cols=6, seed=35)
+    _evict(c, 33, 4, 8)
+
+
+# ---- together, graphs, streams -------------------------------------------------
+
+def test_a_run_of_all_three():
+    """Prompts, then steps of append, decode with weights and, now and then, an
+    eviction: against an fp64 cache of plain lists that does the same."""
+    dev = _dev()
+    B, Hkv, G, d, page, budget, sink, local = 3, 2, 4, 64, 16, 48, 4, 16
+    Hq, cols, n_pages = Hkv * G, 6, 3 * 6
+    g = torch.Generator(device="cuda").manual_seed(40)
+    k = torch.zeros(n_pages, Hkv, page, d, device=dev)
+    v = torch.zeros_like(k)
+    table = torch.randperm(n_pages, generator=g, device=dev).view(B, cols).to(I32)
+    prompts = [50, 1, 31]
+    lengths = torch.tensor(prompts, dtype=I32, device=dev)
+    seen = lengths.clone()
+    pos = torch.zeros(B, Hkv, cols * page, dtype=I32, device=dev)
+    weight = torch.zeros(B, Hkv, cols * page, device=dev)
+    start = torch.tensor([0, 50, 51, 82], dtype=I32, device=dev)
+    kn, vn = (torch.randn(82, Hkv, d, generator=g, device=dev) for _ in range(2))
+    sa.paged_append(sa.PagedCache(k, v, table, lengths, pos, seen), kn, vn, start=start, weight=weight)
+    rows = [[[(f64(kn[i, h]), f64(vn[i, h]), i - int(start[b]), 0.0) for i in range(int(start[b]), int(start[b + 1]))]
+             for h in range(Hkv)] for b in range(B)]
+    evictions = 0
+    for step in range(40):
+        lengths = lengths + 1
+        seen = seen + 1
+        kn, vn = (torch.randn(B, Hkv, d, generator=g, device=dev) for _ in range(2))
+        q = torch.randn(B, Hq, d, generator=g, device=dev) * 2
+        cache = sa.PagedCache(k, v, table, lengths, pos, seen)
+        sa.paged_append(cache, kn, vn, weight=weight)
+        out, lse = sa.paged_decode(q, cache, softcap=15.0, weight=weight, weight_out=weight)
+        evict = step % 9 == 8
+        if evict:
+            lengths, weight, pos = sa.paged_evict(cache, weight, budget, sink, local)
+        torch.cuda.synchronize()
+        for b in range(B):
+            newest = int(seen[b]) - 1
+            for h in range(Hkv):
+                u = rows[b][h]
+                u.append((f64(kn[b, h]), f64(vn[b, h]), newest, 0.0))
+                K, V, P, W = (np.array([t[i] for t in u]) for i in range(4))
+                o, l, p = opaged.decode_unit(f64(q[b, h * G:(h + 1) * G]), K, V, P, newest, np.ones(len(u), dtype=bool),
+                                             1 / math.sqrt(d), 15.0)
+                # the bound of the module's head with |x| < 15: well below 1e-4 of sums of unit normals
+                assert np.abs(f64(out[b, h * G:(h + 1) * G]) - o).max() < 1e-4
+                assert np.abs(f64(lse[b, h * G:(h + 1) * G]) - l).max() < 1e-4
+                W = W + p.sum(axis=0)
+                if evict and len(u) > budget:
+                    evictions += 1
+                    src = opaged.evict_unit(W, P, newest, budget, sink, local)
+                    K, V, P, W = K[src], V[src], P[src], W[src]
+                rows[b][h] = [(K[i], V[i], int(P[i]), W[i]) for i in range(len(P))]
+                n = int(lengths[b])
+                assert n == len(P) and pos[b, h, :n].tolist() == P.tolist()
+                assert np.abs(f64(weight[b, h, :n]) - W).max() < 1e-4 * (step + 2)
+    assert evictions >= 8
+
+
+def test_graphs_follow_lengths_and_do_not_share():
+    """Two captured graphs, replayed in turn and at the same time, with lengths,
+    tables and queries that change between replays."""
+    dev = _dev()
+    cs = [Case([3000, 700], cols=200, seed=50), Case([100, 2500], cols=200, seed=51)]
+    runs = []
+    for c in cs:
+        cache = c.cache()
+        new = torch.randn(c.B, c.Hkv, c.d, device=dev).to(BF)
+        wo = torch.zeros_like(c.weight)
+        out, lse = torch.empty(c.B, c.Hq, c.d, device=dev), torch.empty(c.B, c.Hq, device=dev)
+
+        def step(c=c, cache=cache, new=new, wo=wo, out=out, lse=lse):
+            sa.paged_append(cache, new, new)
+            sa.paged_decode(c.q, cache, weight=c.weight, weight_out=wo, out=out, lse=lse)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        runs.append((c, graph, step, wo, out, lse))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, lens in enumerate(([3000, 700], [1, 64], [3200, 0], [17, 2999])):
+        for c, *_ in runs:
+            c.lengths.copy_(torch.tensor(lens))
+            c.q.copy_(torch.randn(c.q.shape, device=dev).to(BF))
+            # slots never written hold NaN: fill them
+            c.k.nan_to_num_(nan=0.25)
+            c.v.nan_to_num_(nan=0.5)
+        torch.cuda.synchronize()
+        for (c, graph, *_), s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for c, graph, step, wo, out, lse in runs:
+            got = [t.clone() for t in (wo, out, lse)]
+            step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, (wo, out, lse))), i
+            _check_decode(c, out, lse)
+
+
+def test_evict_captured():
+    c = Case([500, 90], seed=52)
+    cache = c.cache()
+    out = sa.paged_evict(cache, c.weight, 64, 4, 8)
+    torch.cuda.synchronize()
+    c = Case([500, 90], seed=52)
+    cache = c.cache()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = sa.paged_evict(cache, c.weight, 64, 4, 8)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, got))
+
+
+def test_streams_side_by_side():
+    """One cache read on several streams at once: no shared scratch."""
+    c = Case([6000, 800, 40], seed=53)
+    cache = c.cache()
+    want = sa.paged_decode(c.q, cache)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for _ in range(8):
+        for s in streams:
+            got.append(sa.paged_decode(c.q, cache, stream=s))
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+# ---- refusals ------------------------------------------------------------------
+
+def test_python_refusals():
+    dev = _dev()
+    c = Case([40, 9], tracked=True, seed=60)
+    cache = c.cache()
+    long_k = c.k.clone().unsqueeze(0)
+    for kw in (dict(pos=None), dict(seen=None), dict(table=c.table.long()), dict(lengths=c.lengths[:1]),
+               dict(lengths=c.lengths.cpu()), dict(k=c.k.float()), dict(k=long_k), dict(v=c.v[:, :1]),
+               dict(pos=c.pos[..., :-1]), dict(k=c.k.half(), v=c.v.half()),
+               dict(k=c.k[..., ::2], v=c.v[..., ::2]), dict(k=c.k[:1].expand_as(c.k), v=c.v[:1].expand_as(c.v)),
+               dict(k=c.k.transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises((ValueError, TypeError)):
+            c.cache(**kw)
+    q = c.q
+    for bad in (q.float(), q[:1], q[..., :64], q[:, :c.Hkv + 1], q.cpu(), q.transpose(0, 1).contiguous().transpose(0, 1)):
+        with pytest.raises((ValueError, sa.SAError)):
+            sa.paged_decode(bad, cache)
+    w = torch.zeros(c.B, c.Hkv, c.cap, device=dev)
+    for kw in (dict(weight=w), dict(weight_out=w[..., :-1]), dict(weight_out=w.double()), dict(slopes=w[0, 0, :3]),
+               dict(out=w), dict(lse=w), dict(scale=-1.0), dict(softcap=-1.0), dict(sink=-1), dict(local=-1),
+               dict(softcap=math.nan)):
+        with pytest.raises((ValueError, sa.SAError)):
+            sa.paged_decode(q, cache, **kw)
+    new = torch.randn(2, c.Hkv, c.d, device=dev).to(BF)
+    for a in ((new.float(), new.float()), (new, new[:1]), (new[:1], new[:1]), (new[..., :64], new[..., :64]),
+              (new, new.transpose(0, 1).contiguous().transpose(0, 1)), (new.cpu(), new.cpu()),
+              (new[:1].expand(2, -1, -1), new[:1].expand(2, -1, -1))):
+        with pytest.raises((ValueError, sa.SAError)):
+            sa.paged_append(cache, *a)
+    with pytest.raises(ValueError):
+        sa.paged_append(cache, new, new, start=torch.zeros(2, dtype=I32, device=dev))
+    for a, kw in (((w, 0), {}), ((w, 8, 5, 4), {}), ((w[..., :-1], 8), {}), ((w, 8), dict(weight_out=w)),
+                  ((w, 8), dict(pos_out=c.pos)), ((w, 8), dict(lengths_out=c.lengths))):
+        with pytest.raises((ValueError, sa.SAError)):
+            sa.paged_evict(cache, *a, **kw)
+    d96 = torch.zeros(4, 2, 16, 96, dtype=BF, device=dev)
+    with pytest.raises(sa.SAError):
+        sa.paged_decode(torch.zeros(2, 2, 96, dtype=BF, device=dev),
+                        sa.PagedCache(d96, d96.clone(), c.table[:, :2].contiguous(), c.lengths))
