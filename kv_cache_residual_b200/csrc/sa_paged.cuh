@@ -16,13 +16,21 @@ __device__ __forceinline__ int pg_newest(const PagedView& c, int b, int len) {
     return (c.seen != nullptr ? __ldg(c.seen + b) : len) - 1;
 }
 
-// element offset of (slot, head) of the sequence whose table row is `trow`,
-// or -1 where its page is not one of the pool
-__device__ __forceinline__ long long pg_row(const PagedView& c, const int32_t* trow, int g, int slot) {
-    const int col = c.shift >= 0 ? slot >> c.shift : slot / c.page;
-    const int page = __ldg(trow + col);
+__device__ __forceinline__ int pg_col(const PagedView& c, int slot) {
+    return c.shift >= 0 ? slot >> c.shift : slot / c.page;
+}
+
+// element offset of (slot, head), its page read from the table before, or -1
+// where that is not one of the pool
+__device__ __forceinline__ long long pg_offset(const PagedView& c, int page, int g, int slot) {
     if ((unsigned)page >= (unsigned)c.n_pages) return -1;
-    return (long long)page * c.ps + (long long)g * c.hs + (long long)(slot - col * c.page) * c.rs;
+    const int row = c.shift >= 0 ? slot & (c.page - 1) : slot % c.page;
+    return (long long)page * c.ps + (long long)g * c.hs + (long long)row * c.rs;
+}
+
+// the same for the sequence whose table row is `trow`
+__device__ __forceinline__ long long pg_row(const PagedView& c, const int32_t* trow, int g, int slot) {
+    return pg_offset(c, __ldg(trow + pg_col(c, slot)), g, slot);
 }
 
 // The slots a query reads, as a list without gaps: all of [0, len), or, where

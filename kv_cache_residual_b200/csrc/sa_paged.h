@@ -11,7 +11,6 @@
 namespace sa {
 
 constexpr int kPgTile = 64;            // slots per tile: the unit of the split over a cache's length
-constexpr int kPgHeads = 8;            // query heads of one unit; wider groups are several units per KV head
 constexpr int kPgSlots = 148 * 2;      // CTAs of the decode: two per SM
 
 struct PagedDims {
@@ -19,7 +18,7 @@ struct PagedDims {
     int bf16;
     int n_pages, page, shift, max_pages;   // shift: log2(page), or -1
     int cap, ldw;                          // slots per sequence, row length of pos and of the weights
-    int nhb;                               // units per KV head
+    int hu, nhb;                           // query heads of a unit (8 or 16), units per KV head
     long long ps, hs, rs;                  // page, head and row strides (elements)
     int U() const { return B * Hkv; }
     int esz() const { return bf16 ? 2 : 4; }
@@ -33,13 +32,13 @@ struct PagedView {
     const int32_t* lengths;
     const int32_t* pos;
     const int32_t* seen;
-    int B, Hq, Hkv, G, nhb;
+    int B, Hq, Hkv, G, hu, nhb;
     int n_pages, page, shift, max_pages, cap, ldw;
     long long ps, hs, rs;
 };
 
 inline PagedView paged_view(const PagedDims& d, const sa_paged_cache& c) {
-    return PagedView{c.k, c.v, c.table, c.lengths, c.pos, c.seen, d.B, d.Hq, d.Hkv, d.G, d.nhb,
+    return PagedView{c.k, c.v, c.table, c.lengths, c.pos, c.seen, d.B, d.Hq, d.Hkv, d.G, d.hu, d.nhb,
                      d.n_pages, d.page, d.shift, d.max_pages, d.cap, d.ldw, d.ps, d.hs, d.rs};
 }
 
@@ -49,7 +48,8 @@ inline PagedView paged_view(const PagedDims& d, const sa_paged_cache& c) {
 // continues, one for the unit it begins.
 struct PagedDecodePlan {
     int grid;
-    int rec;                               // floats per record: m[8], l[8], acc[8][d]
+    int rec;                               // floats per record: m[hu], l[hu], acc[hu][d]
+    int ldx;                               // floats per row of logits
     size_t off_cnt, off_rec, off_lse, off_x, bytes;
 };
 
@@ -57,14 +57,14 @@ inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
     PagedDecodePlan p;
     const long long tiles = (long long)d.U() * d.nhb * ((d.cap + kPgTile - 1) / kPgTile);
     p.grid = (int)(tiles < kPgSlots ? tiles : kPgSlots);
-    p.rec = kPgHeads * (2 + d.d);
+    p.rec = d.hu * (2 + d.d);
+    p.ldx = (d.cap + kPgTile - 1) / kPgTile * kPgTile;
     size_t off = 0;
     p.off_cnt = off; off = align256(off + sizeof(unsigned) * (size_t)d.U() * d.nhb);
     p.off_rec = off; off = align256(off + sizeof(float) * 2 * (size_t)p.grid * p.rec);
-    // with weights: log2 of every row's mass, and the logits (log2) of every
-    // slot, heads of a group side by side
+    // with weights: log2 of every row's mass, and the logits (log2) of its slots
     p.off_lse = off; if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq);
-    p.off_x = off;   if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq * d.cap);
+    p.off_x = off;   if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq * p.ldx);
     p.bytes = off;
     return p;
 }

@@ -28,7 +28,9 @@ sa_status check_paged_shape(const sa_paged_shape* s, PagedDims* d) {
     d->cap = (int)cap;
     d->ldw = s->ldw == 0 ? d->cap : s->ldw;
     if (d->ldw < d->cap) return SA_ERR_INVALID_ARG;
-    d->nhb = (d->G + kPgHeads - 1) / kPgHeads;
+    // the matrix instructions of the bf16 decode take sixteen rows of queries
+    d->hu = d->bf16 && d->G > 8 ? 16 : 8;
+    d->nhb = (d->G + d->hu - 1) / d->hu;
     if ((long long)d->U() * d->nhb * ((d->cap + kPgTile - 1) / kPgTile) >= (1LL << 31)) return SA_ERR_UNSUPPORTED;
     d->ps = s->page_stride; d->hs = s->head_stride; d->rs = s->row_stride;
     if (d->ps == 0 && d->hs == 0 && d->rs == 0) {

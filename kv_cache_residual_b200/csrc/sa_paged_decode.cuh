@@ -15,12 +15,12 @@ struct PgDecodeIo {
     float* out;
     float* lse;
     float* lse2;             // with weights: log2 of the rows' masses
-    float* x;                // with weights: logits (log2) [B, Hkv, cap, G], or null
+    float* x;                // with weights: logits (log2) [B, Hq, ldx] of the listed slots, or null
     float* rec;              // two records per CTA
     unsigned* cnt;           // completion tickets, one per unit
     float scale, qscale;     // softmax scale, and times log2(e)
     float softcap, cap_in, cap_out;    // c, scale / c, c log2(e)
-    int sink, local, min_tiles;
+    int sink, local, min_tiles, ldx;
 };
 
 // logit in log2 units: the dot product scaled, capped (tanhf: 2 ulp, so that
@@ -30,21 +30,32 @@ __device__ __forceinline__ float pg_logit(const PgDecodeIo& io, float dot, float
     return fmaf(-slope2, dist, x);
 }
 
-// Whether the token of a listed slot is visible, its row offset (-1: not) and
-// its distance from the newest position.
-__device__ __forceinline__ long long pg_see(const PgDecodeIo& io, const int32_t* trow, int b, int g, int slot,
-                                            int newest, float& dist) {
-    long long away = (long long)newest - slot;
-    if (io.c.pos != nullptr) {
-        const int p = __ldg(io.c.pos + ((size_t)b * io.c.Hkv + g) * io.c.ldw + slot);
-        away = (long long)newest - p;
-        if (io.local > 0 && !(p < io.sink || away < io.local)) {
-            dist = 0.f;
-            return -1;
-        }
+// What a lane reads of a listed slot: its page, and its position where slots
+// have positions of their own.  Only loads here, so that they can be issued
+// well ahead of pg_see.
+struct PgRaw {
+    int slot, page, pos;
+};
+
+__device__ __forceinline__ PgRaw pg_fetch(const PgDecodeIo& io, const PgList& ls, const int32_t* trow,
+                                          const int32_t* prow, int y, int end) {
+    PgRaw r{0, -1, 0};
+    if (y < end) {
+        r.slot = ls.slot(y);
+        r.page = __ldg(trow + pg_col(io.c, r.slot));
+        if (prow != nullptr) r.pos = __ldg(prow + r.slot);
     }
+    return r;
+}
+
+// the slot's row offset (-1: not visible) and its distance from the newest position
+__device__ __forceinline__ long long pg_see(const PgDecodeIo& io, const PgRaw& r, bool own_pos, int g, int newest,
+                                            float& dist) {
+    const int p = own_pos ? r.pos : r.slot;
+    const long long away = (long long)newest - p;
     dist = (float)away;
-    return pg_row(io.c, trow, g, slot);
+    if (own_pos && io.local > 0 && !(p < io.sink || away < io.local)) return -1;
+    return pg_offset(io.c, r.page, g, r.slot);
 }
 
 // Records of a unit, in split order: its first CTA's second record, then the
@@ -65,12 +76,13 @@ __device__ __forceinline__ void pg_write(const PgDecodeIo& io, size_t qh, int e,
 }
 
 // The unit's last CTA joins its n records (fixed order) and writes the rows of
-// its gh heads.  f: shared scratch of 8 n + 16 floats.
+// its gh of hu heads.  f: shared scratch of hu (n + 2) floats.
 template <int D, int NT>
-__device__ void pg_join(const PgDecodeIo& io, int floats, int first, int n, size_t qh0, int gh, float* f) {
+__device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int gh, float* f) {
+    const int hu = io.c.hu, floats = hu * (2 + D);
     float* sM = f;
-    float* sL = f + kPgHeads;
-    float* w = f + 2 * kPgHeads;               // [head][record] weights 2^(m - M)
+    float* sL = f + hu;
+    float* w = f + 2 * hu;               // [head][record] weights 2^(m - M)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto rec = [&](int s) -> const float* { return pg_rec(io.rec, floats, first + s, s == 0); };
     for (int h = warp; h < gh; h += NT / 32) {
@@ -90,7 +102,7 @@ __device__ void pg_join(const PgDecodeIo& io, int floats, int first, int n, size
             const float m = w[h * n + s];
             const float x = m == -INFINITY ? 0.f : ex2(m - M);
             w[h * n + s] = x;
-            L = fmaf(__ldcg(rec(s) + kPgHeads + h), x, L);
+            L = fmaf(__ldcg(rec(s) + hu + h), x, L);
         }
         L = group_sum<32>(L);
         if (lane == 0) { sM[h] = M; sL[h] = L; }
@@ -101,7 +113,7 @@ __device__ void pg_join(const PgDecodeIo& io, int floats, int first, int n, size
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int s = 0; s < n; ++s) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(rec(s) + 2 * kPgHeads + h * D + e));
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(rec(s) + 2 * hu + h * D + e));
             const float y = w[h * n + s];
             A.x = fmaf(a.x, y, A.x);
             A.y = fmaf(a.y, y, A.y);
