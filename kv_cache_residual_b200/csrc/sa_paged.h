@@ -97,12 +97,12 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedDims& d, const PagedAppendArgs& a, cudaStream_t s);
 
-// Eviction: a cluster of CTAs per (sequence, KV head); scratch: its freed
-// slots and the late kept slots that move into them.
+// Eviction: a cluster of CTAs per (sequence, KV head); scratch: the number of
+// its moves, its freed slots and the late kept slots that move into them.
 struct PagedEvictPlan {
     int cluster, slice_max;                // CTAs per unit, most slots of one
     int moves;                             // most moves of a unit
-    size_t off_list, bytes;
+    size_t off_count, off_list, bytes;
 };
 
 PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget);

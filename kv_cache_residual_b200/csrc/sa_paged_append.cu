@@ -16,6 +16,20 @@ k_paged_append(PagedAppendArgs a, int parts, long long items) {
     const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (item >= items) return;
     const int i = (int)(item / parts), part = (int)(item - (long long)i * parts);
+    // the rows first: they do not wait for the search of where they go
+    const int n = c.Hkv * CPR;
+    const T* kn = static_cast<const T*>(a.k_new) + (long long)i * a.token_stride;
+    const T* vn = static_cast<const T*>(a.v_new) + (long long)i * a.token_stride;
+    uint4 wk[UN], wv[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+        const int x = part * 32 * UN + j * 32 + lane;
+        if (x < n) {
+            const long long o = (long long)(x / CPR) * a.head_stride + (x % CPR) * EPC;
+            wk[j] = ld_stream16(kn + o);
+            wv[j] = ld_stream16(vn + o);
+        }
+    }
     // the token's sequence, and how many of its tokens come from this one on
     int b = i, left = 1;
     if (a.start != nullptr) {
@@ -40,21 +54,8 @@ k_paged_append(PagedAppendArgs a, int parts, long long items) {
     }
     const long long row = pg_row(c, c.table + (size_t)b * c.max_pages, 0, slot);
     if (row < 0) return;
-    const int n = c.Hkv * CPR;
-    const T* kn = static_cast<const T*>(a.k_new) + (long long)i * a.token_stride;
-    const T* vn = static_cast<const T*>(a.v_new) + (long long)i * a.token_stride;
     T* k = static_cast<T*>(const_cast<void*>(c.k)) + row;
     T* v = static_cast<T*>(const_cast<void*>(c.v)) + row;
-    uint4 wk[UN], wv[UN];
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-        const int x = part * 32 * UN + j * 32 + lane;
-        if (x < n) {
-            const long long o = (long long)(x / CPR) * a.head_stride + (x % CPR) * EPC;
-            wk[j] = ld_stream16(kn + o);
-            wv[j] = ld_stream16(vn + o);
-        }
-    }
 #pragma unroll
     for (int j = 0; j < UN; ++j) {
         const int x = part * 32 * UN + j * 32 + lane;

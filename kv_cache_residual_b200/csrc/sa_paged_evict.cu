@@ -5,11 +5,14 @@
 // n' move into the freed slots before it, so sources and destinations never
 // meet and the rows move in place, in any order, in one pass.
 //
-// One cluster of CTAs per unit, each over a slice of the slots: 32-bit keys
-// in shared memory, four 8-bit radix passes whose histograms are summed over
-// the cluster through distributed shared memory, ranks by ballots and prefix
-// sums in slot order, then the moves.  Bound: HBM for the moved rows; for
-// small evictions the chain of cluster barriers.
+// k_evict_select: one cluster of CTAs per unit, each over a slice of the slots.
+// 32-bit keys in shared memory; radix digits of 11, 11 and 10 bits, their
+// histograms summed over the cluster through distributed shared memory, until
+// the digits' prefix alone tells who stays (22 bits mostly do); ranks by
+// ballots and prefix sums in slot order; out come the lists of freed and of
+// late kept slots.  Bound: the chain of barriers.
+// k_evict_move: the rows, split evenly over the GPU whatever the units'
+// counts.  Bound: HBM, each moved row read once and written once.
 #include <cooperative_groups.h>
 
 #include "sa_paged.cuh"
@@ -20,7 +23,10 @@ namespace sa {
 
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvKeys = 48 * 1024;     // most keys of a slice kept in shared memory
+constexpr int kEvBins = 2048;
+constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory
+constexpr int kEvMoveThreads = 256;
+constexpr int kEvMoveUn = 4;           // rows in flight per lane group
 
 // Order of the slots: larger keys stay.  Protected slots first, then the
 // weights as ordered integers (-0 and +0 alike), NaN as -inf.
@@ -31,27 +37,41 @@ __device__ __forceinline__ uint32_t ev_key(float w, bool always) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kEvThreads)
-k_paged_evict(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists) {
-    extern __shared__ uint32_t s_key[];
-    __shared__ uint32_t s_hist[4][256];
-    __shared__ uint32_t s_part[8];
+template <int CL>
+__device__ __forceinline__ void ev_sync() {
+    if constexpr (CL == 1) __syncthreads();
+    else cg::this_cluster().sync();
+}
+
+template <int CL, typename T>
+__device__ __forceinline__ const T* ev_peer(T* p, int rank) {
+    if constexpr (CL == 1) return p;
+    else return cg::this_cluster().map_shared_rank(p, rank);
+}
+
+template <int CL>
+__global__ void __launch_bounds__(kEvThreads, 2)
+k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int32_t* counts) {
+    extern __shared__ __align__(16) uint32_t s_mem[];
+    uint32_t* s_hist = s_mem;                          // [3][kEvBins]
+    uint32_t* s_key = s_mem + 3 * kEvBins;
+    __shared__ uint32_t s_part[kEvWarps];
     __shared__ uint32_t s_digit, s_above, s_equal;
     __shared__ uint32_t s_cnt[3];                      // equal keys, freed slots, late kept slots of this slice
     __shared__ uint32_t s_w[2][kEvWarps];
 
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks();
     const PagedView& c = a.c;
-    const int u = blockIdx.x / CL, b = u / c.Hkv, g = u - b * c.Hkv;
+    const int u = blockIdx.x / CL, rank = blockIdx.x % CL, b = u / c.Hkv, g = u - b * c.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int len = pg_length(c, b), keep = min(len, a.budget);
     const size_t row = (size_t)u * c.ldw;
     const float* W = a.weight + row;
     const int32_t* P = c.pos == nullptr ? nullptr : c.pos + row;
-    if (threadIdx.x == 0 && rank == 0 && g == 0) a.lengths_out[b] = keep;
-    const int slice = (len + CL - 1) / CL;
+    if (threadIdx.x == 0 && rank == 0) {
+        if (g == 0) a.lengths_out[b] = keep;
+        if (len <= a.budget) counts[u] = 0;
+    }
+    const int slice = ((len + CL - 1) / CL + 31) & ~31;
     const int lo = min(len, rank * slice), hi = min(len, lo + slice);
     if (len <= a.budget) {                             // nothing to evict: the whole cluster leaves
         for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) {
@@ -60,6 +80,7 @@ k_paged_evict(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists) {
         }
         return;
     }
+    cudaTriggerProgrammaticLaunchCompletion();         // the moves' CTAs may come and wait
     const long long newest = pg_newest(c, b, len);
     // crowded: more slots hold protected positions than may stay (positions given
     // twice), so that the weights decide among those alone
@@ -71,69 +92,79 @@ k_paged_evict(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists) {
     };
     const bool cached = hi - lo <= slice_keys;
     auto key = [&](int s) -> uint32_t { return cached ? s_key[s - lo] : make_key(s); };
-    uint32_t prefix, need, equal;
-    for (;;) {
-        for (int x = threadIdx.x; x < 4 * 256; x += kEvThreads) (&s_hist[0][0])[x] = 0u;
-        if (cached)
-            for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) s_key[s - lo] = make_key(s);
-        __syncthreads();
 
-        // ---- the smallest kept key: keep-th largest, one digit at a time ----------
-        uint32_t mask = 0u;
-        prefix = 0u;
+    // ---- the digits of the smallest kept key ------------------------------------------
+    // slots with key & mask > prefix stay; of the `equal` slots with key & mask
+    // == prefix the first `need`
+    uint32_t prefix, mask, need, equal;
+    for (;;) {
+        for (int x = threadIdx.x; x < 3 * kEvBins; x += kEvThreads) s_hist[x] = 0u;
+        if (cached) {
+#pragma unroll 4
+            for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) s_key[s - lo] = make_key(s);
+        }
+        __syncthreads();
+        mask = prefix = equal = 0u;
         need = (uint32_t)keep;
-        equal = 0u;
-        for (int d = 0; d < 4; ++d) {
-            const int sh = 24 - 8 * d;
+        for (int d = 0; d < 3 && need != equal; ++d) {
+            const int sh = d == 0 ? 21 : (d == 1 ? 10 : 0);
+            const uint32_t bins = d == 2 ? 1023u : 2047u;
+            uint32_t* h = s_hist + d * kEvBins;
+#pragma unroll 4
             for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) {
                 const uint32_t k = key(s);
-                if ((k & mask) == prefix) atomicAdd(&s_hist[d][(k >> sh) & 255u], 1u);
+                if ((k & mask) == prefix) atomicAdd(h + ((k >> sh) & bins), 1u);
             }
-            cl.sync();
-            // thread t < 256: digit 255 - t over the whole unit, then an inclusive scan
-            uint32_t n = 0u, inc = 0u;
-            if (threadIdx.x < 256) {
-                for (int r = 0; r < CL; ++r) n += cl.map_shared_rank(&s_hist[d][0], r)[255 - threadIdx.x];
-                inc = n;
+            ev_sync<CL>();
+            // thread t: four bins from 2047 - 4 t down, over the whole unit
+            const int top = kEvBins - 4 - 4 * (int)threadIdx.x;
+            uint4 v[CL];
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                if (lane == 31) s_part[warp] = inc;
+            for (int r = 0; r < CL; ++r) v[r] = *reinterpret_cast<const uint4*>(ev_peer<CL>(h, r) + top);
+            uint32_t q[4] = {0u, 0u, 0u, 0u};          // from the top bin down
+#pragma unroll
+            for (int r = 0; r < CL; ++r) { q[0] += v[r].w; q[1] += v[r].z; q[2] += v[r].y; q[3] += v[r].x; }
+            const uint32_t n = q[0] + q[1] + q[2] + q[3];
+            uint32_t inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
+            if (lane == 31) s_part[warp] = inc;
             __syncthreads();
-            if (threadIdx.x < 256) {
-                for (int w = 0; w < warp; ++w) inc += s_part[w];
-                if (inc >= need && inc - n < need) {       // exactly one digit
-                    s_digit = 255u - threadIdx.x;
-                    s_above = inc - n;
-                    s_equal = n;
+#pragma unroll
+            for (int w = 0; w < kEvWarps; ++w) inc += w < warp ? s_part[w] : 0u;
+            uint32_t before = inc - n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {              // the bin that holds the need-th: exactly one
+                if (before < need && before + q[j] >= need) {
+                    s_digit = (uint32_t)(top + 3 - j);
+                    s_above = before;
+                    s_equal = q[j];
                 }
+                before += q[j];
             }
             __syncthreads();
             prefix |= s_digit << sh;
-            mask |= 255u << sh;
+            mask |= bins << sh;
             need -= s_above;
             equal = s_equal;
         }
+        // more protected slots than may stay: only the protected have this key
         if (crowded || prefix != 0xffffffffu || need == equal) break;
         crowded = true;
-        cl.sync();                                     // the histograms have been read by all
+        ev_sync<CL>();                                 // the histograms have been read by all
     }
-    // slots with a larger key stay; of the `equal` slots with key == prefix the
-    // first `need`
 
     // ---- ranks in slot order ---------------------------------------------------------
     // warp w takes a run of the slice, 32 slots at a time
     const int run = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) & ~31;
     const int w0 = min(hi, lo + warp * run), w1 = min(hi, w0 + run);
-    if (threadIdx.x < 3) s_cnt[threadIdx.x] = 0u;
     uint32_t eq_rank = 0u;                             // equal keys in slots before this warp's run
-    __syncthreads();
     if (need < equal) {
         uint32_t n = 0u;
-        for (int s = w0 + lane; s < w1; s += 32) n += key(s) == prefix ? 1u : 0u;
+        for (int s = w0 + lane; s < w1; s += 32) n += (key(s) & mask) == prefix ? 1u : 0u;
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) s_w[0][warp] = n;
         __syncthreads();
@@ -142,30 +173,41 @@ k_paged_evict(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists) {
             for (int w = 0; w < kEvWarps; ++w) t += s_w[0][w];
             s_cnt[0] = t;
         }
-        cl.sync();
-        for (int r = 0; r < rank; ++r) eq_rank += *cl.map_shared_rank(&s_cnt[0], r);
+        ev_sync<CL>();
+#pragma unroll
+        for (int r = 0; r < CL; ++r) {
+            const uint32_t t = *ev_peer<CL>(&s_cnt[0], r);
+            eq_rank += r < rank ? t : 0u;
+        }
         for (int w = 0; w < warp; ++w) eq_rank += s_w[0][w];
         __syncthreads();
     }
-    // calls f(slot, kept) for the warp's slots, 32 at a time, kept meaningful where slot < w1
+    // calls f(slot, whether it is one, whether it stays) for the warp's slots, 32 at a time
     auto each = [&](auto f) {
         uint32_t eq = eq_rank;
         for (int s0 = w0; s0 < w1; s0 += 32) {
             const int s = s0 + lane;
-            const uint32_t k = s < w1 ? key(s) : 0u;
-            bool stays = s < w1 && k > prefix;
-            const bool tie = s < w1 && k == prefix;
-            const unsigned ties = __ballot_sync(0xffffffffu, tie);
-            if (tie) stays = need == equal || eq + __popc(ties & ((1u << lane) - 1u)) < need;
-            eq += __popc(ties);
-            f(s, s < w1, stays);
+            const bool in = s < w1;
+            const uint32_t k = in ? key(s) & mask : 0u;
+            bool stays = in && k > prefix;
+            const bool tie = in && k == prefix;
+            if (need == equal) {
+                stays |= tie;
+            } else {
+                const unsigned ties = __ballot_sync(0xffffffffu, tie);
+                if (tie) stays = eq + __popc(ties & ((1u << lane) - 1u)) < need;
+                eq += __popc(ties);
+            }
+            f(s, in, stays);
         }
     };
     uint32_t nh = 0u, nl = 0u;
     each([&](int s, bool in, bool stays) {
-        nh += __popc(__ballot_sync(0xffffffffu, in && s < keep && !stays));
-        nl += __popc(__ballot_sync(0xffffffffu, in && s >= keep && stays));
+        nh += in && s < keep && !stays ? 1u : 0u;
+        nl += s >= keep && stays ? 1u : 0u;
     });
+    nh = __reduce_add_sync(0xffffffffu, nh);
+    nl = __reduce_add_sync(0xffffffffu, nl);
     if (lane == 0) { s_w[0][warp] = nh; s_w[1][warp] = nl; }
     __syncthreads();
     if (threadIdx.x < 2) {
@@ -173,109 +215,150 @@ k_paged_evict(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists) {
         for (int w = 0; w < kEvWarps; ++w) t += s_w[threadIdx.x][w];
         s_cnt[1 + threadIdx.x] = t;
     }
-    cl.sync();
+    ev_sync<CL>();
     uint32_t hole = 0u, late = 0u, total = 0u;
+#pragma unroll
     for (int r = 0; r < CL; ++r) {
-        const uint32_t* q = cl.map_shared_rank(&s_cnt[0], r);
+        const uint32_t* q = ev_peer<CL>(&s_cnt[0], r);
         const uint32_t h = q[1], l = q[2];
         total += h;
-        if (r < rank) { hole += h; late += l; }
+        hole += r < rank ? h : 0u;
+        late += r < rank ? l : 0u;
     }
+    ev_sync<CL>();                                     // no CTA reads another's memory from here
     for (int w = 0; w < warp; ++w) { hole += s_w[0][w]; late += s_w[1][w]; }
+    if (threadIdx.x == 0 && rank == 0) counts[u] = (int32_t)total;
     int32_t* holes = lists + (size_t)u * 2 * moves;
     int32_t* lates = holes + moves;
     each([&](int s, bool in, bool stays) {
-        const bool h = in && s < keep && !stays, l = in && s >= keep && stays;
+        const bool h = in && s < keep && !stays, l = s >= keep && stays;
         const unsigned mh = __ballot_sync(0xffffffffu, h), ml = __ballot_sync(0xffffffffu, l);
         const unsigned below = (1u << lane) - 1u;
         if (h) holes[hole + __popc(mh & below)] = s;
         if (l) lates[late + __popc(ml & below)] = s;
         hole += __popc(mh);
         late += __popc(ml);
-        if (in && s < keep && stays) {
+        if (s < keep && stays) {
             a.weight_out[row + s] = W[s];
             a.pos_out[row + s] = P == nullptr ? s : P[s];
         }
     });
-    cl.sync();                                         // the lists are whole; no CTA reads another's memory from here
+}
 
-    // ---- the moves --------------------------------------------------------------------
+// CTA x of a unit: its moves [x M, (x + 1) M), M = rows in flight of the CTA.
+template <typename T, int D>
+__global__ void __launch_bounds__(kEvMoveThreads)
+k_evict_move(PagedEvictArgs a, int chunks, int moves, const int32_t* lists, const int32_t* counts) {
     using Gm = Geom<T, D>;
-    constexpr int CPR = Gm::CPR, EPC = Gm::EPC, NG = Gm::GPW * kEvWarps;
-    constexpr int UN = 4;
-    const int li = threadIdx.x % CPR, grp = threadIdx.x / CPR;
+    constexpr int CPR = Gm::CPR, EPC = Gm::EPC, NG = kEvMoveThreads / CPR, M = NG * kEvMoveUn;
+    const PagedView& c = a.c;
+    const int u = blockIdx.x / chunks, m0 = (blockIdx.x - u * chunks) * M, b = u / c.Hkv, g = u - b * c.Hkv;
+    cudaGridDependencySynchronize();                   // the lists
+    const int n = __ldcg(counts + u);
+    if (m0 >= n) return;
+    const size_t row = (size_t)u * c.ldw;
+    const int32_t* holes = lists + (size_t)u * 2 * moves;
+    const int32_t* lates = holes + moves;
     const int32_t* trow = c.table + (size_t)b * c.max_pages;
+    const int li = threadIdx.x % CPR, grp = threadIdx.x / CPR;
     T* K = static_cast<T*>(const_cast<void*>(c.k)) + li * EPC;
     T* V = static_cast<T*>(const_cast<void*>(c.v)) + li * EPC;
-    for (int m0 = (rank * NG + grp) * UN; m0 < (int)total; m0 += CL * NG * UN) {
-        uint4 wk[UN], wv[UN];
-        long long to[UN];
+    int src[kEvMoveUn], dst[kEvMoveUn];
 #pragma unroll
-        for (int j = 0; j < UN; ++j) {
-            to[j] = -1;
-            if (m0 + j < (int)total) {
-                const int src = __ldcg(lates + m0 + j), dst = __ldcg(holes + m0 + j);
-                const long long from = pg_row(c, trow, g, src);
-                to[j] = from < 0 ? -1 : pg_row(c, trow, g, dst);
-                if (to[j] >= 0) {
-                    wk[j] = ld_stream16(K + from);
-                    wv[j] = ld_stream16(V + from);
-                }
-                if (li == 0) {
-                    a.weight_out[row + dst] = W[src];
-                    a.pos_out[row + dst] = P == nullptr ? src : P[src];
-                }
-            }
+    for (int j = 0; j < kEvMoveUn; ++j) {
+        const int m = m0 + j * NG + grp;
+        src[j] = m < n ? __ldcg(lates + m) : -1;
+        dst[j] = m < n ? __ldcg(holes + m) : -1;
+    }
+    long long from[kEvMoveUn], to[kEvMoveUn];
+#pragma unroll
+    for (int j = 0; j < kEvMoveUn; ++j) {
+        from[j] = src[j] < 0 ? -1 : pg_row(c, trow, g, src[j]);
+        to[j] = src[j] < 0 ? -1 : pg_row(c, trow, g, dst[j]);
+    }
+    uint4 wk[kEvMoveUn], wv[kEvMoveUn];
+#pragma unroll
+    for (int j = 0; j < kEvMoveUn; ++j) {
+        if (from[j] >= 0 && to[j] >= 0) {
+            wk[j] = ld_stream16(K + from[j]);
+            wv[j] = ld_stream16(V + from[j]);
         }
+    }
+    for (int m = m0 + threadIdx.x; m < min(n, m0 + M); m += kEvMoveThreads) {
+        const int s = __ldcg(lates + m), d = __ldcg(holes + m);
+        a.weight_out[row + d] = __ldg(a.weight + row + s);
+        a.pos_out[row + d] = c.pos == nullptr ? s : __ldg(c.pos + row + s);
+    }
 #pragma unroll
-        for (int j = 0; j < UN; ++j) {
-            if (to[j] >= 0) {
-                *reinterpret_cast<uint4*>(K + to[j]) = wk[j];
-                *reinterpret_cast<uint4*>(V + to[j]) = wv[j];
-            }
+    for (int j = 0; j < kEvMoveUn; ++j) {
+        if (from[j] >= 0 && to[j] >= 0) {
+            *reinterpret_cast<uint4*>(K + to[j]) = wk[j];
+            *reinterpret_cast<uint4*>(V + to[j]) = wv[j];
         }
     }
 }
 
 PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget) {
     PagedEvictPlan p;
-    // few units: more CTAs each, up to the portable eight
+    // few units: more CTAs each, up to the portable eight, as long as all are
+    // resident at once (two per SM)
     p.cluster = 1;
-    while (p.cluster < 8 && (long long)d.U() * p.cluster < 148 * 2 && d.cap / p.cluster > 1024) p.cluster *= 2;
-    const int slice = cdiv(d.cap, p.cluster);
+    while (p.cluster < 8 && (long long)d.U() * p.cluster * 2 <= 148 * 2 && d.cap / p.cluster > 1024) p.cluster *= 2;
+    const int slice = (cdiv(d.cap, p.cluster) + 31) & ~31;
     p.slice_max = slice < kEvKeys ? slice : kEvKeys;
     const int past = d.cap > budget ? d.cap - budget : 0;
     p.moves = past < budget ? past : budget;
-    if (p.moves < 1) p.moves = 1;
-    p.off_list = 0;
-    p.bytes = align256(sizeof(int32_t) * 2 * (size_t)d.U() * p.moves);
+    size_t off = 0;
+    p.off_count = off; off = align256(off + sizeof(int32_t) * (size_t)d.U());
+    p.off_list = off;  off = align256(off + sizeof(int32_t) * 2 * (size_t)d.U() * p.moves);
+    p.bytes = off;
     return p;
 }
 
-template <typename T, int D>
-static cudaError_t evict_t(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s) {
+template <int CL>
+static cudaError_t select_t(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> opted{0};
-    cudaError_t e = opt_in_smem(k_paged_evict<T, D>, (size_t)kEvKeys * 4, opted);
+    const cudaError_t e = opt_in_smem(k_evict_select<CL>, (size_t)(3 * kEvBins + kEvKeys) * 4, opted);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)d.U() * p.cluster);
+    cfg.gridDim = dim3((unsigned)d.U() * CL);
     cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = (size_t)p.slice_max * 4;
+    cfg.dynamicSmemBytes = (size_t)(3 * kEvBins + p.slice_max) * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.x = CL;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_evict_select<CL>, a, p.slice_max, p.moves,
+                              reinterpret_cast<int32_t*>(a.ws + p.off_list), reinterpret_cast<int32_t*>(a.ws + p.off_count));
+}
+
+template <typename T, int D>
+static cudaError_t move_t(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s) {
+    const int chunks = cdiv(p.moves, kEvMoveThreads / Geom<T, D>::CPR * kEvMoveUn);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)d.U() * chunks);
+    cfg.blockDim = dim3(kEvMoveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_evict<T, D>, a, p.slice_max, p.moves,
-                              reinterpret_cast<int32_t*>(a.ws + p.off_list));
+    return cudaLaunchKernelEx(&cfg, k_evict_move<T, D>, a, chunks, p.moves,
+                              static_cast<const int32_t*>(reinterpret_cast<int32_t*>(a.ws + p.off_list)),
+                              static_cast<const int32_t*>(reinterpret_cast<int32_t*>(a.ws + p.off_count)));
 }
 
 cudaError_t launch_paged_evict(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s) {
-    if (d.bf16) return d.d == 128 ? evict_t<__nv_bfloat16, 128>(d, p, a, s) : evict_t<__nv_bfloat16, 64>(d, p, a, s);
-    return d.d == 128 ? evict_t<float, 128>(d, p, a, s) : evict_t<float, 64>(d, p, a, s);
+    const cudaError_t e = p.cluster == 1 ? select_t<1>(d, p, a, s) : p.cluster == 2 ? select_t<2>(d, p, a, s)
+                        : p.cluster == 4 ? select_t<4>(d, p, a, s) : select_t<8>(d, p, a, s);
+    if (e != cudaSuccess || p.moves == 0) return e;    // no sequence can be longer than the budget
+    if (d.bf16) return d.d == 128 ? move_t<__nv_bfloat16, 128>(d, p, a, s) : move_t<__nv_bfloat16, 64>(d, p, a, s);
+    return d.d == 128 ? move_t<float, 128>(d, p, a, s) : move_t<float, 64>(d, p, a, s);
 }
 
 }  // namespace sa
