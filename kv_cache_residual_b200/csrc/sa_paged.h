@@ -100,9 +100,10 @@ cudaError_t launch_paged_append(const PagedDims& d, const PagedAppendArgs& a, cu
 // Eviction: a cluster of CTAs per (sequence, KV head); scratch: the number of
 // its moves, its freed slots and the late kept slots that move into them.
 struct PagedEvictPlan {
-    int cluster, slice_max;                // CTAs per unit, most slots of one
+    int cluster;                           // CTAs per unit
+    int near_keys;                         // keys of a CTA in shared memory (0: in the workspace)
     int moves;                             // most moves of a unit
-    size_t off_count, off_list, bytes;
+    size_t off_count, off_list, off_keys, bytes;
 };
 
 PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget);

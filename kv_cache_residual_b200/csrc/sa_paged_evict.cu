@@ -6,11 +6,14 @@
 // meet and the rows move in place, in any order, in one pass.
 //
 // k_evict_select: one cluster of CTAs per unit, each over a slice of the slots.
-// 32-bit keys in shared memory; radix digits of 11, 11 and 10 bits, their
-// histograms summed over the cluster through distributed shared memory, until
-// the digits' prefix alone tells who stays (22 bits mostly do); ranks by
-// ballots and prefix sums in slot order; out come the lists of freed and of
-// late kept slots.  Bound: the chain of barriers.
+// One pass over the weights makes 32-bit keys (in shared memory, or in the
+// workspace where a slice is too long) and writes the outputs of the slots that
+// may stay in place.  Then radix digits of 11, 11 and 10 bits until the digits'
+// prefix alone tells who stays (22 bits mostly do): a histogram per CTA, of
+// which the cluster reads 64 coarse sums and then the 32 bins of one of them
+// through distributed shared memory.  Ranks by ballots and prefix sums in slot
+// order; out come the lists of freed and of late kept slots.  Bound: the chain
+// of barriers and the latency of the weights.
 // k_evict_move: the rows, split evenly over the GPU whatever the units'
 // counts.  Bound: HBM, each moved row read once and written once.
 #include <cooperative_groups.h>
@@ -23,7 +26,8 @@ namespace sa {
 
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvBins = 2048;
+constexpr int kEvBins = 2048, kEvCoarse = 64;
+constexpr int kEvUn = 8;               // slots of a thread read at once
 constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory
 constexpr int kEvMoveThreads = 256;
 constexpr int kEvMoveUn = 4;           // rows in flight per lane group
@@ -51,11 +55,10 @@ __device__ __forceinline__ const T* ev_peer(T* p, int rank) {
 
 template <int CL>
 __global__ void __launch_bounds__(kEvThreads, 2)
-k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int32_t* counts) {
+k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uint32_t* far_keys) {
     extern __shared__ __align__(16) uint32_t s_mem[];
     uint32_t* s_hist = s_mem;                          // [3][kEvBins]
-    uint32_t* s_key = s_mem + 3 * kEvBins;
-    __shared__ uint32_t s_part[kEvWarps];
+    __shared__ __align__(8) uint32_t s_coarse[3][kEvCoarse];
     __shared__ uint32_t s_digit, s_above, s_equal;
     __shared__ uint32_t s_cnt[3];                      // equal keys, freed slots, late kept slots of this slice
     __shared__ uint32_t s_w[2][kEvWarps];
@@ -73,25 +76,13 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
     }
     const int slice = ((len + CL - 1) / CL + 31) & ~31;
     const int lo = min(len, rank * slice), hi = min(len, lo + slice);
-    if (len <= a.budget) {                             // nothing to evict: the whole cluster leaves
-        for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) {
-            a.weight_out[row + s] = W[s];
-            a.pos_out[row + s] = P == nullptr ? s : P[s];
-        }
-        return;
-    }
     cudaTriggerProgrammaticLaunchCompletion();         // the moves' CTAs may come and wait
+    const bool evicts = len > a.budget;
     const long long newest = pg_newest(c, b, len);
+    uint32_t* keys = far_keys == nullptr ? s_mem + 3 * kEvBins : far_keys + (size_t)u * c.cap + lo;
     // crowded: more slots hold protected positions than may stay (positions given
     // twice), so that the weights decide among those alone
     bool crowded = false;
-    auto make_key = [&](int s) -> uint32_t {
-        const long long p = P == nullptr ? s : __ldg(P + s);
-        const bool always = p < a.sink || newest - p < a.local;
-        return crowded ? (always ? ev_key(__ldg(W + s), false) : 0u) : ev_key(__ldg(W + s), always);
-    };
-    const bool cached = hi - lo <= slice_keys;
-    auto key = [&](int s) -> uint32_t { return cached ? s_key[s - lo] : make_key(s); };
 
     // ---- the digits of the smallest kept key ------------------------------------------
     // slots with key & mask > prefix stay; of the `equal` slots with key & mask
@@ -99,10 +90,37 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
     uint32_t prefix, mask, need, equal;
     for (;;) {
         for (int x = threadIdx.x; x < 3 * kEvBins; x += kEvThreads) s_hist[x] = 0u;
-        if (cached) {
-#pragma unroll 4
-            for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) s_key[s - lo] = make_key(s);
+        __syncthreads();
+        for (int s0 = lo + threadIdx.x; s0 < hi; s0 += kEvUn * kEvThreads) {
+            float w[kEvUn];
+            int p[kEvUn];
+#pragma unroll
+            for (int j = 0; j < kEvUn; ++j) {
+                const int s = s0 + j * kEvThreads;
+                if (s < hi) {
+                    w[j] = __ldg(W + s);
+                    p[j] = P == nullptr ? s : __ldg(P + s);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kEvUn; ++j) {
+                const int s = s0 + j * kEvThreads;
+                if (s < hi) {
+                    // a freed slot's are written over by the move into it
+                    if (s < keep) {
+                        a.weight_out[row + s] = w[j];
+                        a.pos_out[row + s] = p[j];
+                    }
+                    if (evicts) {
+                        const bool always = p[j] < a.sink || newest - p[j] < a.local;
+                        const uint32_t k = crowded && !always ? 0u : ev_key(w[j], always && !crowded);
+                        keys[s - lo] = k;
+                        atomicAdd(s_hist + (k >> 21), 1u);
+                    }
+                }
+            }
         }
+        if (!evicts) return;                           // the whole cluster
         __syncthreads();
         mask = prefix = equal = 0u;
         need = (uint32_t)keep;
@@ -110,40 +128,58 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
             const int sh = d == 0 ? 21 : (d == 1 ? 10 : 0);
             const uint32_t bins = d == 2 ? 1023u : 2047u;
             uint32_t* h = s_hist + d * kEvBins;
-#pragma unroll 4
-            for (int s = lo + threadIdx.x; s < hi; s += kEvThreads) {
-                const uint32_t k = key(s);
-                if ((k & mask) == prefix) atomicAdd(h + ((k >> sh) & bins), 1u);
+            if (d > 0) {
+                for (int s0 = threadIdx.x; s0 < hi - lo; s0 += kEvUn * kEvThreads) {
+                    uint32_t k[kEvUn];
+#pragma unroll
+                    for (int j = 0; j < kEvUn; ++j) k[j] = s0 + j * kEvThreads < hi - lo ? keys[s0 + j * kEvThreads] : ~prefix;
+#pragma unroll
+                    for (int j = 0; j < kEvUn; ++j)
+                        if ((k[j] & mask) == prefix) atomicAdd(h + ((k[j] >> sh) & bins), 1u);
+                }
+                __syncthreads();
+            }
+            for (int x = warp; x < kEvCoarse; x += kEvWarps) {
+                const uint32_t n = __reduce_add_sync(0xffffffffu, h[x * 32 + lane]);
+                if (lane == 0) s_coarse[d][x] = n;
             }
             ev_sync<CL>();
-            // thread t: four bins from 2047 - 4 t down, over the whole unit
-            const int top = kEvBins - 4 - 4 * (int)threadIdx.x;
-            uint4 v[CL];
+            if (warp == 0) {
+                // from the top: lane l has coarse bins 63 - 2 l and 62 - 2 l of the unit
+                uint32_t q0 = 0u, q1 = 0u;
 #pragma unroll
-            for (int r = 0; r < CL; ++r) v[r] = *reinterpret_cast<const uint4*>(ev_peer<CL>(h, r) + top);
-            uint32_t q[4] = {0u, 0u, 0u, 0u};          // from the top bin down
-#pragma unroll
-            for (int r = 0; r < CL; ++r) { q[0] += v[r].w; q[1] += v[r].z; q[2] += v[r].y; q[3] += v[r].x; }
-            const uint32_t n = q[0] + q[1] + q[2] + q[3];
-            uint32_t inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            if (lane == 31) s_part[warp] = inc;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kEvWarps; ++w) inc += w < warp ? s_part[w] : 0u;
-            uint32_t before = inc - n;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {              // the bin that holds the need-th: exactly one
-                if (before < need && before + q[j] >= need) {
-                    s_digit = (uint32_t)(top + 3 - j);
-                    s_above = before;
-                    s_equal = q[j];
+                for (int r = 0; r < CL; ++r) {
+                    const uint2 y = *reinterpret_cast<const uint2*>(ev_peer<CL>(&s_coarse[d][0], r) + 62 - 2 * lane);
+                    q0 += y.y;
+                    q1 += y.x;
                 }
-                before += q[j];
+                uint32_t inc = q0 + q1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                // the first lane that reaches `need` has the bin
+                const int at = __ffs(__ballot_sync(0xffffffffu, inc >= need)) - 1;
+                uint32_t above = __shfl_sync(0xffffffffu, inc - q0 - q1, at);
+                const uint32_t first = __shfl_sync(0xffffffffu, q0, at);
+                int x = 63 - 2 * at;
+                if (above + first < need) { above += first; --x; }
+                uint32_t n = 0u;                       // lane l: bin 31 - l of coarse bin x
+#pragma unroll
+                for (int r = 0; r < CL; ++r) n += ev_peer<CL>(h, r)[x * 32 + 31 - lane];
+                inc = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                const int bin = __ffs(__ballot_sync(0xffffffffu, above + inc >= need)) - 1;
+                if (lane == bin) {
+                    s_digit = (uint32_t)(x * 32 + 31 - lane);
+                    s_above = above + inc - n;
+                    s_equal = n;
+                }
             }
             __syncthreads();
             prefix |= s_digit << sh;
@@ -164,7 +200,8 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
     uint32_t eq_rank = 0u;                             // equal keys in slots before this warp's run
     if (need < equal) {
         uint32_t n = 0u;
-        for (int s = w0 + lane; s < w1; s += 32) n += (key(s) & mask) == prefix ? 1u : 0u;
+#pragma unroll 4
+        for (int s = w0 + lane; s < w1; s += 32) n += (keys[s - lo] & mask) == prefix ? 1u : 0u;
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) s_w[0][warp] = n;
         __syncthreads();
@@ -184,21 +221,27 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
     }
     // calls f(slot, whether it is one, whether it stays) for the warp's slots, 32 at a time
     auto each = [&](auto f) {
+        constexpr int UN = 4;
         uint32_t eq = eq_rank;
-        for (int s0 = w0; s0 < w1; s0 += 32) {
-            const int s = s0 + lane;
-            const bool in = s < w1;
-            const uint32_t k = in ? key(s) & mask : 0u;
-            bool stays = in && k > prefix;
-            const bool tie = in && k == prefix;
-            if (need == equal) {
-                stays |= tie;
-            } else {
-                const unsigned ties = __ballot_sync(0xffffffffu, tie);
-                if (tie) stays = eq + __popc(ties & ((1u << lane) - 1u)) < need;
-                eq += __popc(ties);
+        for (int s0 = w0; s0 < w1; s0 += 32 * UN) {
+            uint32_t k[UN];
+#pragma unroll
+            for (int j = 0; j < UN; ++j) k[j] = s0 + 32 * j + lane < w1 ? keys[s0 + 32 * j + lane - lo] & mask : 0u;
+#pragma unroll
+            for (int j = 0; j < UN; ++j) {
+                const int s = s0 + 32 * j + lane;
+                const bool in = s < w1;
+                bool stays = in && k[j] > prefix;
+                const bool tie = in && k[j] == prefix;
+                if (need == equal) {
+                    stays |= tie;
+                } else {
+                    const unsigned ties = __ballot_sync(0xffffffffu, tie);
+                    if (tie) stays = eq + __popc(ties & ((1u << lane) - 1u)) < need;
+                    eq += __popc(ties);
+                }
+                f(s, in, stays);
             }
-            f(s, in, stays);
         }
     };
     uint32_t nh = 0u, nl = 0u;
@@ -225,7 +268,6 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
         hole += r < rank ? h : 0u;
         late += r < rank ? l : 0u;
     }
-    ev_sync<CL>();                                     // no CTA reads another's memory from here
     for (int w = 0; w < warp; ++w) { hole += s_w[0][w]; late += s_w[1][w]; }
     if (threadIdx.x == 0 && rank == 0) counts[u] = (int32_t)total;
     int32_t* holes = lists + (size_t)u * 2 * moves;
@@ -238,11 +280,8 @@ k_evict_select(PagedEvictArgs a, int slice_keys, int moves, int32_t* lists, int3
         if (l) lates[late + __popc(ml & below)] = s;
         hole += __popc(mh);
         late += __popc(ml);
-        if (s < keep && stays) {
-            a.weight_out[row + s] = W[s];
-            a.pos_out[row + s] = P == nullptr ? s : P[s];
-        }
     });
+    if constexpr (CL > 1) ev_sync<CL>();               // no CTA leaves while another reads its memory
 }
 
 // CTA x of a unit: its moves [x M, (x + 1) M), M = rows in flight of the CTA.
@@ -305,12 +344,13 @@ PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget) {
     p.cluster = 1;
     while (p.cluster < 8 && (long long)d.U() * p.cluster * 2 <= 148 * 2 && d.cap / p.cluster > 1024) p.cluster *= 2;
     const int slice = (cdiv(d.cap, p.cluster) + 31) & ~31;
-    p.slice_max = slice < kEvKeys ? slice : kEvKeys;
+    p.near_keys = slice <= kEvKeys ? slice : 0;
     const int past = d.cap > budget ? d.cap - budget : 0;
     p.moves = past < budget ? past : budget;
     size_t off = 0;
     p.off_count = off; off = align256(off + sizeof(int32_t) * (size_t)d.U());
     p.off_list = off;  off = align256(off + sizeof(int32_t) * 2 * (size_t)d.U() * p.moves);
+    p.off_keys = off;  if (p.near_keys == 0) off = align256(off + sizeof(uint32_t) * (size_t)d.U() * d.cap);
     p.bytes = off;
     return p;
 }
@@ -323,7 +363,7 @@ static cudaError_t select_t(const PagedDims& d, const PagedEvictPlan& p, const P
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)d.U() * CL);
     cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = (size_t)(3 * kEvBins + p.slice_max) * 4;
+    cfg.dynamicSmemBytes = (size_t)(3 * kEvBins + p.near_keys) * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -332,8 +372,9 @@ static cudaError_t select_t(const PagedDims& d, const PagedEvictPlan& p, const P
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CL > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_evict_select<CL>, a, p.slice_max, p.moves,
-                              reinterpret_cast<int32_t*>(a.ws + p.off_list), reinterpret_cast<int32_t*>(a.ws + p.off_count));
+    return cudaLaunchKernelEx(&cfg, k_evict_select<CL>, a, p.moves,
+                              reinterpret_cast<int32_t*>(a.ws + p.off_list), reinterpret_cast<int32_t*>(a.ws + p.off_count),
+                              p.near_keys > 0 ? nullptr : reinterpret_cast<uint32_t*>(a.ws + p.off_keys));
 }
 
 template <typename T, int D>
