@@ -489,15 +489,18 @@ def append(k_new, v_new, k, v, stats, length, scale=0.0, stream=None):
 
 # ---- the paged cache -----------------------------------------------------------
 
+# A serving loop calls these once per layer and token, so the checks on a call's
+# way are few attribute reads and the scratch is found without asking the library.
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _dense(t, name, dtype, shape, device):
-    """t is a contiguous tensor of this type, shape and device."""
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-          "%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+    """t is a contiguous tensor of this type, shape (a torch.Size or tuple) and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
     return t.data_ptr()
 
 
@@ -523,6 +526,8 @@ class PagedCache:
         self.B, self.max_pages = table.shape
         self.capacity = self.max_pages * self.page
         self.dtype, self.device = k.dtype, k.device
+        self.slots = torch.Size((self.B, self.Hkv, self.capacity))      # of pos and of the weights
+        self._ws = {}
         self.k, self.v, self.table, self.lengths, self.pos, self.seen = k, v, table, lengths, pos, seen
         strides = []
         for t in (k, v):
@@ -545,11 +550,6 @@ class PagedCache:
                                      self.max_pages, 0, *strides[0])
         self._byref = (ctypes.byref(self._shape), ctypes.byref(c))
 
-    @property
-    def slots(self):
-        """Shape of pos and of the weights: [B, Hkv, slots of a sequence]."""
-        return self.B, self.Hkv, self.capacity
-
     def _for_heads(self, Hq):
         """The C shape with Hq query heads."""
         s = self._shape
@@ -567,51 +567,75 @@ class _On:
     __slots__ = ("stream", "guard")
 
     def __init__(self, device, stream):
-        self.guard = None
         if stream is not None:
             _need(stream.device == device, "the stream is on another device than the tensors")
             self.guard = torch.cuda.stream(stream)
-            self.stream = stream
+            self.stream = stream.cuda_stream
         else:
-            self.stream = torch.cuda.current_stream(device)
-            if torch.cuda.current_device() != device.index:
-                self.guard = torch.cuda.device(device)
+            self.guard = torch.cuda.device(device)
+            self.stream = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
+        self.guard.__enter__()
+        return self.stream
 
     def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+        self.guard.__exit__(*e)
         return False
+
+
+def _on_stream(f):
+    """f(stream handle, cache, ...) as a call f(cache, ..., stream=None) on the
+    cache's device."""
+    def call(cache, stream, *args):
+        index = cache.device.index
+        if stream is None and torch.cuda.current_device() == index:
+            return f(torch._C._cuda_getCurrentRawStream(index), cache, *args)
+        with _On(cache.device, stream) as s:
+            return f(s, cache, *args)
+    return call
 
 
 _PAGED_WS = {}
 
 
-def _paged_workspace(shape, op, arg, device, stream):
+def _paged_workspace(cache, Hq, op, arg, stream):
     """Scratch of a paged call with its tickets zeroed, kept per (device, stream,
     op, size, tickets): calls on one stream follow one another, calls on two
     never share it.  A call that is being captured gets its own, whose tickets
     the graph zeroes at each replay, so that graphs replayed side by side do not
     share it either."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing:
+        ws = cache._ws.get((op, arg, Hq, stream))
+        if ws is not None:
+            return ws
+    shape = cache._for_heads(Hq)
     n = _lib().sa_paged_workspace_size(ctypes.byref(shape), op, arg)
     if n == 0:
         raise SAError(SA_ERR_INVALID_ARG, "sa_paged_workspace_size")
     # two shapes of one size can have their records where the other has tickets
-    tickets = 4 * shape.B * shape.Hkv * -(-shape.Hq // (8 * shape.Hkv)) if op == OP_PAGED_DECODE else 0
-    capturing = torch.cuda.is_current_stream_capturing()
-    key = (device.index, stream, op, n, tickets)
-    ws = None if capturing else _PAGED_WS.get(key)
-    if ws is None:
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    tickets = 4 * cache.B * cache.Hkv * -(-Hq // (8 * cache.Hkv)) if op == OP_PAGED_DECODE else 0
+    key = (cache.device.index, stream, op, n, tickets)
+    t = None if capturing else _PAGED_WS.get(key)
+    if t is None:
+        t = torch.empty(n, dtype=torch.uint8, device=cache.device)
         if tickets:
-            ws[:tickets].zero_()
+            t[:tickets].zero_()
         if not capturing:
-            _PAGED_WS[key] = ws
+            _PAGED_WS[key] = t
+    ws = (shape, ctypes.byref(shape), t.data_ptr(), n, t)
+    if not capturing:
+        cache._ws[(op, arg, Hq, stream)] = ws
     return ws
+
+
+@_on_stream
+def _append(s, cache, k_new, v_new, ts, hs, start, weight):
+    status = _lib().sa_paged_append(*cache._byref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, start, k_new.shape[0],
+                                    weight, s)
+    if status != SA_OK:
+        _check(status, "sa_paged_append")
 
 
 def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
@@ -621,23 +645,41 @@ def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
     [B + 1] int32: where each sequence's tokens begin in them (None: one token
     each).  cache.lengths (and cache.seen) already count them.  cache.pos and
     weight [B, Hkv, capacity] f32, where given, are set for the new slots."""
-    _need(k_new.dim() == 3 and k_new.shape[1:] == (cache.Hkv, cache.d) and k_new.shape == v_new.shape and
-          k_new.dtype == v_new.dtype == cache.dtype and k_new.device == v_new.device == cache.device,
-          "k_new and v_new must be [N, Hkv, d] in the cache's type, on its device")
-    N, ts, hs = k_new.shape[0], k_new.stride(0), k_new.stride(1)
+    shape, dtype, device = k_new.shape, cache.dtype, cache.device
+    if not (len(shape) == 3 and shape[1] == cache.Hkv and shape[2] == cache.d and v_new.shape == shape and
+            k_new.dtype is dtype and v_new.dtype is dtype and k_new.device == device and v_new.device == device):
+        raise ValueError("k_new and v_new must be [N, Hkv, d] in the cache's type, on its device")
+    N = shape[0]
+    ts, hs, es = k_new.stride()
+    vt, vh, ve = v_new.stride()
+    # a dimension of size one has no stride of its own
     if cache.Hkv == 1:
-        hs = cache.d
-    if N == 1:
-        ts = hs * cache.Hkv
-    _need(N == 0 or (k_new.stride(2) == 1 and v_new.stride(2) == 1 and
-                     (N == 1 or (v_new.stride(0) == ts and ts > 0)) and
-                     (cache.Hkv == 1 or (v_new.stride(1) == hs and hs > 0))),
-          "k_new and v_new must have contiguous rows and the same strides")
-    ps = None if start is None else _dense(start, "start", torch.int32, (cache.B + 1,), cache.device)
-    pw = None if weight is None else _dense(weight, "weight", torch.float32, cache.slots, cache.device)
-    with _On(cache.device, stream) as s:
-        _check(_lib().sa_paged_append(*cache._byref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, ps, N, pw, s),
-               "sa_paged_append")
+        hs = vh = cache.d
+    if N <= 1:
+        ts = vt = hs * cache.Hkv
+    if not (es == ve == 1 and ts == vt > 0 and hs == vh > 0):
+        raise ValueError("k_new and v_new must have contiguous rows and the same strides")
+    if start is not None:
+        start = _dense(start, "start", torch.int32, (cache.B + 1,), device)
+    if weight is not None:
+        weight = _dense(weight, "weight", torch.float32, cache.slots, device)
+    _append(cache, stream, k_new, v_new, ts, hs, start, weight)
+
+
+@_on_stream
+def _decode(s, cache, q, p, Hq, weights, out, lse):
+    shape = (cache.B, Hq, cache.d)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=cache.device)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
+    po = _dense(out, "out", torch.float32, shape, cache.device)
+    pl = _dense(lse, "lse", torch.float32, shape[:2], cache.device)
+    ws = _paged_workspace(cache, Hq, OP_PAGED_DECODE, weights, s)
+    status = _lib().sa_paged_decode(ws[1], cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl, ws[2], ws[3], s)
+    if status != SA_OK:
+        _check(status, "sa_paged_decode")
+    return out, lse
 
 
 def paged_decode(q, cache, scale=0.0, softcap=0.0, sink=0, local=0, slopes=None, weight=None, weight_out=None,
@@ -650,29 +692,44 @@ def paged_decode(q, cache, scale=0.0, softcap=0.0, sink=0, local=0, slopes=None,
     capacity] f32: weight (None: 0; may be weight_out itself) plus this step's
     attention weights summed over each KV head's query heads.  Returns (out
     [B, Hq, d], lse [B, Hq]), fp32."""
-    _need(q.dim() == 3 and q.shape[0] == cache.B and q.shape[2] == cache.d and q.dtype == cache.dtype and
-          q.device == cache.device, "q must be [B, Hq, d] in the cache's type, on its device")
-    B, Hq, d = q.shape
+    shape, dev = q.shape, cache.device
+    if not (len(shape) == 3 and shape[0] == cache.B and shape[2] == cache.d and q.dtype is cache.dtype and q.device == dev):
+        raise ValueError("q must be [B, Hq, d] in the cache's type, on its device")
+    B, Hq, d = shape
     _need(Hq > 0 and Hq % cache.Hkv == 0, "the query heads must be a multiple of the KV heads")
-    qs = q.stride(0) if B > 1 else Hq * d
-    _need(q.stride(2) == 1 and (Hq == 1 or q.stride(1) == d) and qs > 0,
-          "the heads of a sequence's query must be dense")
-    dev = cache.device
-    f32 = torch.float32
-    shape = cache._for_heads(Hq)
-    _need(weight is None or weight_out is not None, "weight needs weight_out")
-    p = sa_paged_params(float(scale), float(softcap), int(sink), int(local),
-                        None if slopes is None else _dense(slopes, "slopes", f32, (Hq,), dev),
-                        None if weight is None else _dense(weight, "weight", f32, cache.slots, dev),
-                        None if weight_out is None else _dense(weight_out, "weight_out", f32, cache.slots, dev), qs)
-    with _On(dev, stream) as s:
-        out = torch.empty(B, Hq, d, dtype=f32, device=dev) if out is None else out
-        lse = torch.empty(B, Hq, dtype=f32, device=dev) if lse is None else lse
-        po, pl = _dense(out, "out", f32, (B, Hq, d), dev), _dense(lse, "lse", f32, (B, Hq), dev)
-        ws = _paged_workspace(shape, OP_PAGED_DECODE, int(weight_out is not None), dev, s)
-        _check(_lib().sa_paged_decode(ctypes.byref(shape), cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl,
-                                      ws.data_ptr(), ws.numel(), s), "sa_paged_decode")
-    return out, lse
+    qs, qh, qe = q.stride()
+    if B == 1:
+        qs = Hq * d
+    _need(qe == 1 and (Hq == 1 or qh == d) and qs > 0, "the heads of a sequence's query must be dense")
+    _need(-1 < sink < 2 ** 31 and -1 < local < 2 ** 31, "sink and local must be int32, not negative")
+    p = sa_paged_params(float(scale), float(softcap), int(sink), int(local), None, None, None, qs)
+    if slopes is not None:
+        p.slopes = _dense(slopes, "slopes", torch.float32, (Hq,), dev)
+    if weight_out is not None:
+        p.weight_out = _dense(weight_out, "weight_out", torch.float32, cache.slots, dev)
+    if weight is not None:
+        _need(weight_out is not None, "weight needs weight_out")
+        p.weight = _dense(weight, "weight", torch.float32, cache.slots, dev)
+    return _decode(cache, stream, q, p, Hq, weight_out is not None, out, lse)
+
+
+@_on_stream
+def _evict(s, cache, weight, budget, sink, local, lengths_out, weight_out, pos_out):
+    dev, slots = cache.device, cache.slots
+    if lengths_out is None:
+        lengths_out = torch.empty(cache.B, dtype=torch.int32, device=dev)
+    if weight_out is None:
+        weight_out = torch.zeros(slots, dtype=torch.float32, device=dev)
+    if pos_out is None:
+        pos_out = torch.zeros(slots, dtype=torch.int32, device=dev)
+    po = (_dense(lengths_out, "lengths_out", torch.int32, (cache.B,), dev),
+          _dense(weight_out, "weight_out", torch.float32, slots, dev),
+          _dense(pos_out, "pos_out", torch.int32, slots, dev))
+    ws = _paged_workspace(cache, cache.Hkv, OP_PAGED_EVICT, budget, s)
+    status = _lib().sa_paged_evict(*cache._byref, weight, budget, sink, local, *po, ws[2], ws[3], s)
+    if status != SA_OK:
+        _check(status, "sa_paged_evict")
+    return lengths_out, weight_out, pos_out
 
 
 def paged_evict(cache, weight, budget, sink=0, local=0, lengths_out=None, weight_out=None, pos_out=None, stream=None):
@@ -686,22 +743,10 @@ def paged_evict(cache, weight, budget, sink=0, local=0, lengths_out=None, weight
 
     where seen counts the tokens each sequence ever had (before the first
     eviction: the old lengths).  The pages past the new lengths are free."""
-    dev = cache.device
-    pw = _dense(weight, "weight", torch.float32, cache.slots, dev)
-    shape = cache._shape
-    with _On(dev, stream) as s:
-        i32 = dict(dtype=torch.int32, device=dev)
-        lengths_out = torch.empty(cache.B, **i32) if lengths_out is None else lengths_out
-        weight_out = torch.zeros(cache.slots, dtype=torch.float32, device=dev) if weight_out is None else weight_out
-        pos_out = torch.zeros(cache.slots, **i32) if pos_out is None else pos_out
-        po = (_dense(lengths_out, "lengths_out", torch.int32, (cache.B,), dev),
-              _dense(weight_out, "weight_out", torch.float32, cache.slots, dev),
-              _dense(pos_out, "pos_out", torch.int32, cache.slots, dev))
-        _need(0 < int(budget) < 2 ** 31, "budget must be a positive int32")
-        ws = _paged_workspace(shape, OP_PAGED_EVICT, int(budget), dev, s)
-        _check(_lib().sa_paged_evict(*cache._byref, pw, int(budget), int(sink), int(local), *po, ws.data_ptr(),
-                                     ws.numel(), s), "sa_paged_evict")
-    return lengths_out, weight_out, pos_out
+    weight = _dense(weight, "weight", torch.float32, cache.slots, cache.device)
+    _need(0 < budget < 2 ** 31, "budget must be a positive int32")
+    _need(-1 < sink < 2 ** 31 and -1 < local < 2 ** 31, "sink and local must be int32, not negative")
+    return _evict(cache, stream, weight, int(budget), int(sink), int(local), lengths_out, weight_out, pos_out)
 
 
 def wait_timeouts():
