@@ -50,30 +50,38 @@ struct PgUnit {
     }
 };
 
-// Hands in this CTA's part of a unit, own = m[HB], l[HB], acc[HB][D] in shared
-// memory: written out where the CTA has the whole unit, else a record, and the
-// last CTA of the unit joins them (f: hu (n + 2) floats).  All threads call.
-template <typename T, int D, int HB, int NT>
-__device__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgCursor& cur, const PgUnit<T, D>& u,
-                           const float* own, float* f) {
-    const int gh = u.gh, hu = io.c.hu;
-    if (cur.tile == 0 && u.end == u.nt) {
-        for (int x = threadIdx.x; x < gh * D; x += NT) {
-            const int h = x / D, e = x - h * D;
-            pg_write<D>(io, u.qh0 + h, e, own[2 * HB + x], own[h], own[HB + h]);
+// This CTA's part of a unit: written out where the CTA has the whole unit, else
+// a record, which the last CTA of the unit joins with the others.
+template <typename T, int D>
+struct PgPart {
+    bool whole;
+    float* rec;
+    __device__ __forceinline__ PgPart(const PgDecodeIo& io, const PgCursor& cur, const PgUnit<T, D>& u)
+        : whole(cur.tile == 0 && u.end == u.nt), rec(pg_rec(io.rec, io.c.hu * (2 + D), blockIdx.x, cur.tile == 0)) {}
+    // accumulator A of dim e of head h, mass L relative to 2^M
+    __device__ __forceinline__ void put(const PgDecodeIo& io, const PgUnit<T, D>& u, int h, int e, float A, float M,
+                                        float L) const {
+        if (whole) {
+            pg_write<D>(io, u.qh0 + h, e, A, M, L);
+        } else {
+            rec[2 * io.c.hu + h * D + e] = A;
+            if (e == 0) { rec[h] = M; rec[io.c.hu + h] = L; }
         }
-        return;
     }
-    float* r = pg_rec(io.rec, hu * (2 + D), blockIdx.x, cur.tile == 0);
-    for (int x = threadIdx.x; x < gh * (D + 2); x += NT) {
-        if (x < gh) r[x] = own[x];
-        else if (x < 2 * gh) r[hu + x - gh] = own[HB + x - gh];
-        else r[2 * hu + x - 2 * gh] = own[2 * HB + x - 2 * gh];
-    }
+};
+
+// after all have put: the unit's last CTA joins.  All threads call; f as pg_join.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgCursor& cur,
+                                           const PgUnit<T, D>& u, const PgPart<T, D>& part, float* f) {
+    if (part.whole) return;
     const int first = sp.owner(cur.unit0), n = sp.owner(cur.unit0 + u.nt - 1) - first + 1;
     unsigned* cnt = io.cnt + (size_t)cur.b * io.c.Hkv * io.c.nhb + cur.sub;
     if (last_cta_of_unit(cnt, n)) {
-        pg_join<D, NT>(io, first, n, u.qh0, gh, f);
+        for (int h0 = 0; h0 < u.gh; h0 += 8) {
+            pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f);
+            __syncthreads();
+        }
         reset_counter(cnt);
     }
 }
@@ -105,18 +113,12 @@ template <int D>
 struct PgStage {
     static constexpr int kPitch = 2 * D + 16;
     static constexpr int kBytes = 2 * 16 * kPitch + 16 * 4;      // K rows, V rows, distances
-    static constexpr int kStages = D == 128 ? 3 : 6;             // 8 KB of rows in flight per warp and stage pair
+    static constexpr int kStages = D == 128 ? 3 : 5;             // with the scratch, what two CTAs per SM have room for
+    static constexpr int kRing = kPtWarps * kStages * kBytes;
+    static constexpr int kAcc = kPtWarps * 4 * (D + 4);          // floats: four heads' states of the warps
+    static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
+    static constexpr size_t kSmem = kRing + 4 * (size_t)kScratch;
 };
-
-template <int D, int HB>
-__host__ __device__ constexpr size_t pg_tc_smem() {
-    const size_t ring = (size_t)kPtWarps * PgStage<D>::kStages * PgStage<D>::kBytes;
-    // over the ring: the warps' states, the CTA's, or the join's weights
-    const size_t merge = sizeof(float) * ((size_t)kPtWarps * HB * (D + 4 + 2) + HB * (D + 2));
-    const size_t join = sizeof(float) * (HB == 16 ? 16 : 8) * (kPgSlots + 2);
-    const size_t m = merge > join ? merge : join;
-    return ring > m ? ring : m;
-}
 
 __device__ __forceinline__ void pg_cp16(uint32_t s, const void* g, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(ok ? 16 : 0) : "memory");
@@ -133,71 +135,85 @@ __device__ __forceinline__ void split3(float p0, float p1, uint32_t& hi, uint32_
 template <int D, int HB>
 __global__ void __launch_bounds__(kPtThreads, 2)
 k_paged_tc(PgDecodeIo io) {
+    using T = __nv_bfloat16;
     using St = PgStage<D>;
     constexpr int S = St::kStages, P = St::kPitch;
     constexpr int KS = D / 16, MT = D / 16;
     constexpr int CPR = D / 8, RPI = 32 / CPR;                   // chunks per row, rows per copy instruction
     constexpr int R = HB == 16 ? 2 : 1;                          // query rows per lane
+    constexpr int LD = D + 4;
     extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float s_ml[kPtWarps][HB][2];
     const PagedView& c = io.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
     const int per = c.Hkv * c.nhb;
-    unsigned char* ring = smem + (size_t)warp * S * St::kBytes;
+    unsigned char* ring = smem + warp * S * St::kBytes;
+    float* scratch = reinterpret_cast<float*>(smem + St::kRing);
     const uint32_t ring_u = tc::smem_u32(ring);
+    const T* K = static_cast<const T*>(c.k) + (lane % CPR) * 8;
+    const T* V = static_cast<const T*>(c.v) + (lane % CPR) * 8;
     PgSplit sp;
     PgCursor cur;
     long long t0, t1;
+    cudaTriggerProgrammaticLaunchCompletion();                   // the weights' kernel may come and wait
     if (!pg_locate<kPtThreads>(c.B, per, io.min_tiles, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
-    while (t0 < t1) {
-        const PgUnit<__nv_bfloat16, D> u(io, cur, t1 - t0);
-        const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(c.k) + (lane % CPR) * 8;
-        const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(c.v) + (lane % CPR) * 8;
-        // this warp's steps: 16 list entries from row0 + i kPgTile
-        const int row0 = cur.tile * kPgTile + warp * 16;
-        const int n = u.s1 > row0 ? (u.s1 - row0 + kPgTile - 1) / kPgTile : 0;
-        const bool own_pos = u.prow != nullptr;
-        auto fetch = [&](int i) { return pg_fetch(io, u.ls, u.trow, u.prow, row0 + i * kPgTile + (lane & 15), i < n ? u.s1 : 0); };
-        auto issue = [&](int i, const PgRaw& raw) {
-            float dist;
-            const long long off = pg_see(io, raw, own_pos, u.g, u.newest, dist);
-            const uint32_t base = ring_u + (uint32_t)(i % S) * St::kBytes;
-            if (lane < 16)
-                *reinterpret_cast<float*>(ring + (i % S) * St::kBytes + 32 * P + 4 * lane) = off >= 0 ? dist : INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16 / RPI; ++j) {
-                const int row = j * RPI + lane / CPR;
-                const long long o = __shfl_sync(0xffffffffu, off, row);
-                const uint32_t at = base + row * P + (lane % CPR) * 16;
-                pg_cp16(at, K + (o < 0 ? 0 : o), o >= 0);
-                pg_cp16(at + 16 * P, V + (o < 0 ? 0 : o), o >= 0);
-            }
-        };
-        {
-            PgRaw raw[S - 1];
-#pragma unroll
-            for (int i = 0; i < S - 1; ++i) raw[i] = fetch(i);
-#pragma unroll
-            for (int i = 0; i < S - 1; ++i) {
-                if (i < n) issue(i, raw[i]);
-                tc::cp_commit();
-            }
-        }
-        PgRaw ahead = fetch(S - 1);
+    int head[R], stage = 0;                                       // ring stage of the unit's first step
+    uint32_t qa[KS][2 * R];
+    float sl[R];
+    PgRaw ahead;
+    PgUnit<T, D> u(io, cur, t1 - t0);
+    int row0, n;                                                  // this warp's steps: 16 list entries from row0 + i kPgTile
 
-        uint32_t qa[KS][2 * R];
-        float sl[R], m[R], l[R], o[R][MT][4];
-        int head[R];
+    auto fetch = [&](int i) {
+        return pg_fetch(io, u.ls, u.trow, u.prow, row0 + i * kPgTile + (lane & 15), i < n ? u.s1 : 0);
+    };
+    auto issue = [&](int i, const PgRaw& raw) {
+        float dist;
+        const long long off = pg_see(io, raw, u.prow != nullptr, u.g, u.newest, dist);
+        const int at = (stage + i) % S * St::kBytes;
+        if (lane < 16) *reinterpret_cast<float*>(ring + at + 32 * P + 4 * lane) = off >= 0 ? dist : INFINITY;
+#pragma unroll
+        for (int j = 0; j < 16 / RPI; ++j) {
+            const int row = j * RPI + lane / CPR;
+            const long long o = __shfl_sync(0xffffffffu, off, row);
+            const uint32_t to = ring_u + at + row * P + (lane % CPR) * 16;
+            pg_cp16(to, K + (o < 0 ? 0 : o), o >= 0);
+            pg_cp16(to + 16 * P, V + (o < 0 ? 0 : o), o >= 0);
+        }
+    };
+    // a unit's queries and the copies of its first steps; runs while the unit
+    // before it is handed in
+    auto begin = [&]() {
+        row0 = cur.tile * kPgTile + warp * 16;
+        n = u.s1 > row0 ? (u.s1 - row0 + kPgTile - 1) / kPgTile : 0;
+        PgRaw raw[S - 1];
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) raw[i] = fetch(i);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             head[k] = HB == 4 ? (r & 3) : r + 8 * k;
             sl[k] = u.slope2(io, head[k]);
-            const __nv_bfloat16* q = u.q + (size_t)head[k] * D + 2 * t;
+            const T* q = u.q + (size_t)head[k] * D + 2 * t;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                qa[ks][k] = head[k] < u.gh ? *reinterpret_cast<const uint32_t*>(q + ks * 16) : 0u;
-                qa[ks][R + k] = head[k] < u.gh ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8) : 0u;
+                qa[ks][k] = head[k] < u.gh ? __ldg(reinterpret_cast<const unsigned*>(q + ks * 16)) : 0u;
+                qa[ks][R + k] = head[k] < u.gh ? __ldg(reinterpret_cast<const unsigned*>(q + ks * 16 + 8)) : 0u;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            if (i < n) issue(i, raw[i]);
+            tc::cp_commit();
+        }
+        ahead = fetch(S - 1);
+    };
+    begin();
+
+    for (;;) {
+        float m[R], l[R], o[R][MT][4];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
             m[k] = -INFINITY;
             l[k] = 0.f;
 #pragma unroll
@@ -205,7 +221,6 @@ k_paged_tc(PgDecodeIo io) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[k][mt][j] = 0.f;
         }
-
         for (int i = 0; i < n; ++i) {
             __syncwarp();                                         // stage i - 1 has been read by all lanes
             if (i + S - 1 < n) issue(i + S - 1, ahead);
@@ -213,8 +228,9 @@ k_paged_tc(PgDecodeIo io) {
             ahead = fetch(i + S);
             tc::cp_wait<S - 1>();
             __syncwarp();
-            const uint32_t kt = ring_u + (uint32_t)(i % S) * St::kBytes, vt = kt + 16 * P;
-            const float* dist = reinterpret_cast<const float*>(ring + (i % S) * St::kBytes + 32 * P);
+            const int at = (stage + i) % S * St::kBytes;
+            const uint32_t kt = ring_u + at, vt = kt + 16 * P;
+            const float* dist = reinterpret_cast<const float*>(ring + at + 32 * P);
             float s[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -302,54 +318,63 @@ k_paged_tc(PgDecodeIo io) {
                 }
             }
         }
-        tc::cp_wait<0>();
-        __syncthreads();                                          // the ring is free: states over it
-
-        constexpr int LD = D + 4;
-        float* acc = reinterpret_cast<float*>(smem);              // [warp][HB][LD]
-        float* ml = acc + kPtWarps * HB * LD;                     // [warp][HB][2]
-        float* own = ml + kPtWarps * HB * 2;                      // m[HB], l[HB], acc[HB][D]
+        __syncwarp();
+        // the unit is done: its successor's first copies go out before it is handed in
+        const PgUnit<T, D> done = u;
+        const PgCursor at = cur;
+        t0 += u.end - cur.tile;
+        const bool more = t0 < t1;
+        stage = (stage + n) % S;
+        if (more) {
+            pg_next(cur, per, u.nt);
+            u = PgUnit<T, D>(io, cur, t1 - t0);
+            begin();
+        }
+        const PgPart<T, D> part(io, at, done);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
             l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
             if (t == 0 && (HB != 4 || r < 4)) {
-                ml[(warp * HB + head[k]) * 2] = m[k];
-                ml[(warp * HB + head[k]) * 2 + 1] = l[k];
+                s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][0] = m[k];
+                s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][1] = l[k];
             }
+        }
+        // four heads at a time through the scratch
+#pragma unroll
+        for (int hq = 0; hq < HB / 4; ++hq) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float y = o[k][mt][j];
-                    if (HB == 4) y += __shfl_xor_sync(0xffffffffu, y, 2);
-                    const int h = 2 * t + (j & 1) + 8 * k;
-                    if (HB != 4 || t < 2) acc[(warp * HB + h) * LD + mt * 16 + r + (j >> 1) * 8] = y;
+                    float y = o[hq / 2][mt][j];
+                    if (HB == 4) y += __shfl_xor_sync(0xffffffffu, y, 2);        // its parts' two columns
+                    if (t / 2 == (hq & 1))
+                        scratch[(warp * 4 + (2 * t + (j & 1)) % 4) * LD + mt * 16 + r + (j >> 1) * 8] = y;
                 }
-        }
-        __syncthreads();
-        for (int x = threadIdx.x; x < u.gh * D; x += kPtThreads) {
-            const int h = x / D, e = x - h * D;
-            float M = -INFINITY, A = 0.f, L = 0.f;
+            __syncthreads();
+            for (int x = threadIdx.x; x < 4 * D; x += kPtThreads) {
+                const int h4 = x / D, e = x - h4 * D, h = 4 * hq + h4;
+                if (h >= done.gh) break;
+                float M = -INFINITY, A = 0.f, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kPtWarps; ++w) M = fmaxf(M, ml[(w * HB + h) * 2]);
+                for (int w = 0; w < kPtWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
 #pragma unroll
-            for (int w = 0; w < kPtWarps; ++w) {
-                const float mw = ml[(w * HB + h) * 2];
-                const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-                A = fmaf(acc[(w * HB + h) * LD + e], f, A);
-                L = fmaf(ml[(w * HB + h) * 2 + 1], f, L);
+                for (int w = 0; w < kPtWarps; ++w) {
+                    const float mw = s_ml[w][h][0];
+                    const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+                    A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
+                    L = fmaf(s_ml[w][h][1], f, L);
+                }
+                part.put(io, done, h, e, A, M, L);
             }
-            own[2 * HB + x] = A;
-            if (e == 0) { own[h] = M; own[HB + h] = L; }
+            __syncthreads();
         }
+        pg_hand_in<T, D, kPtThreads>(io, sp, at, done, part, scratch);
+        if (!more) break;
         __syncthreads();
-        // the join's scratch lies over the warps' states: own has been written out by then
-        pg_hand_in<__nv_bfloat16, D, HB, kPtThreads>(io, sp, cur, u, own, acc);
-        __syncthreads();
-        t0 += u.end - cur.tile;
-        pg_next(cur, per, u.nt);
     }
+    tc::cp_wait<0>();
 }
 
 // ---- fp32: CUDA cores --------------------------------------------------------------
@@ -364,7 +389,7 @@ k_paged_cc(PgDecodeIo io) {
     constexpr int UN = 4;                      // rows in flight per lane group
     __shared__ float sm[kWarps * GB * (D + 2)];
     __shared__ float s_own[GB * (D + 2)];
-    __shared__ float s_join[8 * (kPgSlots + 2)];
+    __shared__ __align__(16) float s_join[kPgJoinFloats];
     const PagedView& c = io.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int li = lane % CPR, gsub = lane / CPR;
@@ -372,6 +397,7 @@ k_paged_cc(PgDecodeIo io) {
     PgSplit sp;
     PgCursor cur;
     long long t0, t1;
+    cudaTriggerProgrammaticLaunchCompletion();
     if (!pg_locate<kThreads>(c.B, per, io.min_tiles, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
     while (t0 < t1) {
@@ -423,7 +449,12 @@ k_paged_cc(PgDecodeIo io) {
         }
         warp_merge<GB, EPC, CPR>(os);
         cta_merge_store<GB, EPC, CPR, D>(os, sm, s_own);         // m[GB], l[GB], acc[GB][D]
-        pg_hand_in<T, D, GB, kThreads>(io, sp, cur, u, s_own, s_join);
+        const PgPart<T, D> part(io, cur, u);
+        for (int x = threadIdx.x; x < u.gh * D; x += kThreads) {
+            const int h = x / D, e = x - h * D;
+            part.put(io, u, h, e, s_own[2 * GB + x], s_own[h], s_own[GB + h]);
+        }
+        pg_hand_in<T, D, kThreads>(io, sp, cur, u, part, s_join);
         __syncthreads();
         t0 += u.end - cur.tile;
         pg_next(cur, per, u.nt);
@@ -431,9 +462,11 @@ k_paged_cc(PgDecodeIo io) {
 }
 
 // weight_out = weight + the step's attention weights summed over the group's
-// heads, from the logits the decode left and the rows' masses.  One thread per
-// slot; bound: HBM (or L2, where the logits still are) for 4 G + 8 bytes a slot.
-constexpr int kPgWTile = 1024;         // slots per CTA step
+// heads, from the logits the decode left and the rows' masses.  Four slots per
+// thread, four heads' loads of each at once; bound: HBM (or L2, where the logits
+// still are) for 4 G + 8 bytes a slot.
+constexpr int kPgWUn = 4;
+constexpr int kPgWTile = kThreads * kPgWUn;        // slots per CTA step
 
 __global__ void __launch_bounds__(kThreads)
 k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
@@ -442,26 +475,42 @@ k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
     PgSplit sp;
     PgCursor cur;
     long long t0, t1;
-    if (!pg_locate<kThreads>(c.B, c.Hkv, 1, blockIdx.x, tiles, sp, cur, t0, t1)) return;
+    const bool any = pg_locate<kThreads>(c.B, c.Hkv, 1, blockIdx.x, tiles, sp, cur, t0, t1);
+    cudaGridDependencySynchronize();               // the logits and masses
+    if (!any) return;
     for (long long t = t0; t < t1; ++t) {
         const int b = cur.b, g = cur.sub;
         const PgList ls = pg_list(c, b, io.sink, io.local);
-        const size_t u = (size_t)b * c.Hkv + g;
-        const float* xs = io.x + ((size_t)b * c.Hq + (size_t)g * c.G) * io.ldx;
-        const float* l2 = io.lse2 + (size_t)b * c.Hq + (size_t)g * c.G;
-        const int s1 = min(ls.len, (cur.tile + 1) * kPgWTile), gap = ls.len - ls.n;
-        for (int slot = cur.tile * kPgWTile + threadIdx.x; slot < s1; slot += kThreads) {
-            float p = 0.f;
-            if (slot < ls.s_eff || slot >= ls.s_eff + gap) {
-                const float* x = xs + (slot < ls.s_eff ? slot : slot - gap);
-#pragma unroll 4
-                for (int h = 0; h < c.G; ++h) {
-                    const float y = __ldcg(x + (size_t)h * io.ldx);
-                    p += y == -INFINITY ? 0.f : ex2(y - __ldg(l2 + h));
-                }
+        const size_t u = (size_t)b * c.Hkv + g, row = u * c.ldw;
+        const size_t qh0 = (size_t)b * c.Hq + (size_t)g * c.G;
+        const int gap = ls.len - ls.n, first = cur.tile * kPgWTile + threadIdx.x;
+        float p[kPgWUn], w[kPgWUn];
+        int y[kPgWUn];                             // list entry, -1: not listed
+#pragma unroll
+        for (int j = 0; j < kPgWUn; ++j) {
+            const int slot = first + j * kThreads;
+            y[j] = slot >= ls.len ? -1 : slot < ls.s_eff ? slot : slot >= ls.s_eff + gap ? slot - gap : -1;
+            w[j] = slot < ls.len && weight != nullptr ? weight[row + slot] : 0.f;
+            p[j] = 0.f;
+        }
+        for (int h = 0; h < c.G; h += 4) {
+            float x[4][kPgWUn], l2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                l2[k] = h + k < c.G ? __ldcg(io.lse2 + qh0 + h + k) : 0.f;
+                const float* xs = io.x + (qh0 + h + k) * io.ldx;
+#pragma unroll
+                for (int j = 0; j < kPgWUn; ++j) x[k][j] = h + k < c.G && y[j] >= 0 ? __ldcg(xs + y[j]) : -INFINITY;
             }
-            const size_t w = u * c.ldw + slot;
-            weight_out[w] = (weight == nullptr ? 0.f : weight[w]) + p;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < kPgWUn; ++j) p[j] += x[k][j] == -INFINITY ? 0.f : ex2(x[k][j] - l2[k]);
+        }
+#pragma unroll
+        for (int j = 0; j < kPgWUn; ++j) {
+            const int slot = first + j * kThreads;
+            if (slot < ls.len) weight_out[row + slot] = w[j] + p[j];
         }
         const int nt = tiles(b);
         if (++cur.tile == nt) {
@@ -474,7 +523,7 @@ k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
 template <int D, int HB>
 static cudaError_t tc_launch(const PagedDecodePlan& p, const PgDecodeIo& io, cudaStream_t s) {
     static std::atomic<unsigned long long> opted{0};
-    constexpr size_t smem = pg_tc_smem<D, HB>();
+    constexpr size_t smem = PgStage<D>::kSmem;
     const cudaError_t e = opt_in_smem(k_paged_tc<D, HB>, smem, opted);
     if (e != cudaSuccess) return e;
     k_paged_tc<D, HB><<<p.grid, kPtThreads, smem, s>>>(io);
@@ -520,9 +569,16 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     const cudaError_t e = d.d == 128 ? decode_launch<128>(d, p, io, s) : decode_launch<64>(d, p, io, s);
     if (e != cudaSuccess || !weights) return e;
     const long long steps = (long long)d.U() * ((d.cap + kPgWTile - 1) / kPgWTile);
-    const unsigned grid = (unsigned)(steps < 148 * 8 ? steps : 148 * 8);
-    k_paged_weights<<<grid, kThreads, 0, s>>>(io, a.weight, a.weight_out);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(steps < 148 * 8 ? steps : 148 * 8));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_paged_weights, io, a.weight, a.weight_out);
 }
 
 }  // namespace sa

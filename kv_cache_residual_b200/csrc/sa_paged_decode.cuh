@@ -76,55 +76,94 @@ __device__ __forceinline__ void pg_write(const PgDecodeIo& io, size_t qh, int e,
 }
 
 // The unit's last CTA joins its n records (fixed order) and writes the rows of
-// its gh of hu heads.  f: shared scratch of hu (n + 2) floats.
+// its gh <= 8 heads from h0 on.  Thread (column, part): a column is four dims of
+// a head, and the records are cut into as many parts as there are threads for;
+// a part's first records are on their way before the weights are known.
+// f: shared scratch of kPgJoinFloats floats.  All threads call.
+constexpr int kPgJoin = 12;                // records of a part in flight
+// the heads' m and l, then [head][record] weights, then over them the parts' sums (a float4 per thread)
+constexpr int kPgJoinFloats = 8 * (kPgSlots + 2);
+
 template <int D, int NT>
-__device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int gh, float* f) {
+__device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
     const int hu = io.c.hu, floats = hu * (2 + D);
     float* sM = f;
-    float* sL = f + hu;
-    float* w = f + 2 * hu;               // [head][record] weights 2^(m - M)
+    float* sL = f + 8;
+    float* w = f + 16;                         // [head][record] weights 2^(m - M)
+    float4* sums = reinterpret_cast<float4*>(w);
+    static_assert(16 + 4 * NT <= kPgJoinFloats, "the parts' sums lie over the weights");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto rec = [&](int s) -> const float* { return pg_rec(io.rec, floats, first + s, s == 0); };
-    for (int h = warp; h < gh; h += NT / 32) {
-        float M = -INFINITY;
-        for (int s = lane; s < n; s += 32) {
-            const float m = __ldcg(rec(s) + h);
-            w[h * n + s] = m;
-            M = (m > M || m != m) ? m : M;
-        }
+    auto rec = [&](int s) -> const float* { return pg_rec(io.rec, floats, first + s, s == 0) + h0; };
+    const int cols = gh * (D / 4);
+    const int parts = max(1, NT / cols);
+    const int part = threadIdx.x / cols;       // >= parts: none
+    const int each = (n + parts - 1) / parts;
+    for (int c0 = 0; c0 < cols; c0 += NT) {
+        const int col = c0 + (parts > 1 ? threadIdx.x % cols : threadIdx.x);
+        const int h = col / (D / 4), e = (col % (D / 4)) * 4;
+        const int s0 = parts > 1 ? part * each : 0, s1 = min(n, s0 + each);
+        const bool mine = col < cols && (parts == 1 || part < parts);
+        float4 a[kPgJoin];
+        auto load = [&](int s) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float y = __shfl_xor_sync(0xffffffffu, M, o);
-            M = (y > M || y != y) ? y : M;
+            for (int j = 0; j < kPgJoin; ++j)
+                a[j] = mine && s + j < s1 ? __ldcg(reinterpret_cast<const float4*>(rec(s + j) - h0 + 2 * hu + (h0 + h) * D + e))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        load(s0);
+        if (c0 == 0) {
+            for (int x = warp; x < gh; x += NT / 32) {
+                float M = -INFINITY;
+                for (int s = lane; s < n; s += 32) {
+                    const float m = __ldcg(rec(s) + x);
+                    w[x * n + s] = m;
+                    M = (m > M || m != m) ? m : M;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float y = __shfl_xor_sync(0xffffffffu, M, o);
+                    M = (y > M || y != y) ? y : M;
+                }
+                float L = 0.f;
+                for (int s = lane; s < n; s += 32) {
+                    const float m = w[x * n + s];
+                    const float y = m == -INFINITY ? 0.f : ex2(m - M);
+                    w[x * n + s] = y;
+                    L = fmaf(__ldcg(rec(s) + hu + x), y, L);
+                }
+                L = group_sum<32>(L);
+                if (lane == 0) { sM[x] = M; sL[x] = L; }
+            }
+            __syncthreads();
         }
-        float L = 0.f;
-        for (int s = lane; s < n; s += 32) {
-            const float m = w[h * n + s];
-            const float x = m == -INFINITY ? 0.f : ex2(m - M);
-            w[h * n + s] = x;
-            L = fmaf(__ldcg(rec(s) + hu + h), x, L);
-        }
-        L = group_sum<32>(L);
-        if (lane == 0) { sM[h] = M; sL[h] = L; }
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < gh * (D / 4); x += NT) {
-        const int h = x / (D / 4), e = (x % (D / 4)) * 4;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int s = 0; s < n; ++s) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(rec(s) + 2 * hu + h * D + e));
-            const float y = w[h * n + s];
-            A.x = fmaf(a.x, y, A.x);
-            A.y = fmaf(a.y, y, A.y);
-            A.z = fmaf(a.z, y, A.z);
-            A.w = fmaf(a.w, y, A.w);
+        for (int s = s0; mine && s < s1; s += kPgJoin) {
+            if (s > s0) load(s);
+#pragma unroll
+            for (int j = 0; j < kPgJoin; ++j) {
+                const float y = s + j < s1 ? w[h * n + s + j] : 0.f;
+                A.x = fmaf(a[j].x, y, A.x);
+                A.y = fmaf(a[j].y, y, A.y);
+                A.z = fmaf(a[j].z, y, A.z);
+                A.w = fmaf(a[j].w, y, A.w);
+            }
         }
-        const float M = sM[h], L = sL[h];
-        pg_write<D>(io, qh0 + h, e, A.x, M, L);
-        pg_write<D>(io, qh0 + h, e + 1, A.y, M, L);
-        pg_write<D>(io, qh0 + h, e + 2, A.z, M, L);
-        pg_write<D>(io, qh0 + h, e + 3, A.w, M, L);
+        if (parts > 1) {
+            __syncthreads();
+            if (mine) sums[threadIdx.x] = A;
+            __syncthreads();
+            for (int p = 1; part == 0 && p < parts; ++p) {
+                const float4 B = sums[p * cols + col];
+                A.x += B.x; A.y += B.y; A.z += B.z; A.w += B.w;
+            }
+        }
+        if (mine && (parts == 1 || part == 0)) {
+            const float M = sM[h], L = sL[h];
+            pg_write<D>(io, qh0 + h, e, A.x, M, L);
+            pg_write<D>(io, qh0 + h, e + 1, A.y, M, L);
+            pg_write<D>(io, qh0 + h, e + 2, A.z, M, L);
+            pg_write<D>(io, qh0 + h, e + 3, A.w, M, L);
+        }
     }
 }
 
