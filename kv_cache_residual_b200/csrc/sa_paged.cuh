@@ -17,14 +17,14 @@ __device__ __forceinline__ int pg_newest(const PagedView& c, int b, int len) {
 }
 
 __device__ __forceinline__ int pg_col(const PagedView& c, int slot) {
-    return c.shift >= 0 ? slot >> c.shift : slot / c.page;
+    return (int)((__umulhi((unsigned)slot, c.pmul) + (unsigned)slot) >> c.pshr);
 }
 
 // element offset of (slot, head), its page read from the table before, or -1
 // where that is not one of the pool
 __device__ __forceinline__ long long pg_offset(const PagedView& c, int page, int g, int slot) {
     if ((unsigned)page >= (unsigned)c.n_pages) return -1;
-    const int row = c.shift >= 0 ? slot & (c.page - 1) : slot % c.page;
+    const int row = slot - pg_col(c, slot) * c.page;
     return (long long)page * c.ps + (long long)g * c.hs + (long long)row * c.rs;
 }
 
@@ -52,65 +52,75 @@ __device__ __forceinline__ PgList pg_list(const PagedView& c, int b, int sink, i
     return l;
 }
 
-// The even split: sequence b has tiles(b) tiles in each of its `per` units;
-// all T tiles, in order (sequence, unit, tile), are cut into N ranges [T i / N,
-// T (i + 1) / N).  Every CTA reads all the lengths and sums them, so that no
-// host code or earlier kernel has to know them.
+// The even split: sequence b has tiles(b) tiles in each of its `per` units; all
+// tiles, in order (sequence, unit, tile), are cut into N ranges, the first
+// T % N of them one longer.  A unit costs a CTA more than its tiles (queries,
+// table, merge, hand-in), so every unit counts `extra` tiles more, before its
+// own; T < 2^31 is their number with these.  Every CTA reads all the lengths
+// and sums them, so that no host code or earlier kernel has to know them.
 struct PgSplit {
-    long long T;
-    int N;
-    __device__ __forceinline__ long long begin(int i) const { return T * i / N; }
+    unsigned q, r;           // T / N, T % N
+    int extra;
+    __device__ __forceinline__ unsigned begin(unsigned i) const { return i * q + min(i, r); }
     // the range that tile t lies in
-    __device__ __forceinline__ int owner(long long t) const { return (int)(((t + 1) * N - 1) / T); }
+    __device__ __forceinline__ unsigned owner(unsigned t) const {
+        const unsigned longer = r * (q + 1);
+        return t < longer ? t / (q + 1) : r + (t - longer) / q;
+    }
 };
 
 struct PgCursor {
-    int b, sub, tile;        // sequence, unit within it, tile within the unit
-    long long unit0;         // flat index of the unit's first tile
+    int b, sub, tile;        // sequence, unit within it, tile within the unit, its extra ones first
+    unsigned unit0;          // flat index of the unit's first tile
 };
 
-// Sets split and the cursor of CTA i's first tile (every thread of the CTA
-// calls; NT threads).  min_tiles: fewest tiles worth a CTA.  Returns false
-// where the CTA has no tiles.
+// Sets split, the cursor of CTA i's first tile and its range [t0, t1) (every
+// thread of the CTA calls; NT threads).  The extra tiles are at most a quarter
+// of a CTA's own.  Returns false where the CTA has no tiles.
 template <int NT, typename F>
-__device__ __forceinline__ bool pg_locate(int B, int per, int min_tiles, int i, F tiles, PgSplit& sp, PgCursor& cur,
-                                          long long& t0, long long& t1) {
+__device__ __forceinline__ bool pg_locate(int B, int per, int extra, unsigned i, F tiles, PgSplit& sp, PgCursor& cur,
+                                          unsigned& t0, unsigned& t1) {
     constexpr int W = NT / 32;
-    __shared__ long long s_warp[W];
-    __shared__ long long s_base;
+    __shared__ unsigned s_warp[W];
+    __shared__ unsigned s_base;
     __shared__ int s_b;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int each = (B + NT - 1) / NT;
     const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
-    long long sum = 0;
+    unsigned sum = 0;
     for (int b = b0; b < b1; ++b) sum += tiles(b);
-    long long inc = sum;
+    unsigned inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    long long before = 0, all = 0;
+    unsigned before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const long long y = s_warp[w];
+        const unsigned y = s_warp[w];
         if (w < warp) before += y;
         all += y;
     }
     before += inc - sum;
-    sp.T = all * per;
-    const long long most = sp.T / min_tiles;
-    sp.N = (int)(most < 1 ? 1 : (most < (long long)gridDim.x ? most : (long long)gridDim.x));
-    if (i >= sp.N) return false;               // uniform over the CTA
+    const unsigned N = min(all * (unsigned)per, gridDim.x);
+    if (i >= N) return false;                  // uniform over the CTA
+    const int E = min(extra, (int)(all * (unsigned)per / N) / 4);
+    const unsigned T = (all + (unsigned)(E * B)) * per;
+    sp.extra = E;
+    sp.q = T / N;
+    sp.r = T - sp.q * N;
     t0 = sp.begin(i);
     t1 = sp.begin(i + 1);
+    before += E * b0;
+    sum += E * (b1 - b0);
     if (t0 >= before * per && t0 < (before + sum) * per) {      // this thread's sequences hold t0
-        long long base = before;
+        unsigned base = before;
         int b = b0;
         for (;; ++b) {
-            const int n = tiles(b);
+            const unsigned n = tiles(b) + E;
             if (t0 < (base + n) * per) break;
             base += n;
         }
@@ -119,10 +129,9 @@ __device__ __forceinline__ bool pg_locate(int B, int per, int min_tiles, int i, 
     }
     __syncthreads();
     cur.b = s_b;
-    const int n = tiles(cur.b);
-    const long long r = t0 - s_base * per;
-    cur.sub = (int)(r / n);
-    cur.tile = (int)(r - (long long)cur.sub * n);
+    const unsigned n = tiles(cur.b) + E, x = t0 - s_base * per;
+    cur.sub = (int)(x / n);
+    cur.tile = (int)(x - cur.sub * n);
     cur.unit0 = t0 - cur.tile;
     return true;
 }

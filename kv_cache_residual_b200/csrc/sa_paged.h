@@ -11,12 +11,13 @@
 namespace sa {
 
 constexpr int kPgTile = 64;            // slots per tile: the unit of the split over a cache's length
-constexpr int kPgSlots = 148 * 2;      // CTAs of the decode: two per SM
+constexpr int kPgSlots = 148 * 2;      // most CTAs of the decode
 
 struct PagedDims {
     int B, Hq, Hkv, G, d;
     int bf16;
-    int n_pages, page, shift, max_pages;   // shift: log2(page), or -1
+    int n_pages, page, max_pages;
+    uint32_t pmul, pshr;                   // slot / page = (umulhi(slot, pmul) + slot) >> pshr
     int cap, ldw;                          // slots per sequence, row length of pos and of the weights
     int hu, nhb;                           // query heads of a unit (8 or 16), units per KV head
     long long ps, hs, rs;                  // page, head and row strides (elements)
@@ -33,31 +34,40 @@ struct PagedView {
     const int32_t* pos;
     const int32_t* seen;
     int B, Hq, Hkv, G, hu, nhb;
-    int n_pages, page, shift, max_pages, cap, ldw;
+    int n_pages, page, max_pages, cap, ldw;
+    uint32_t pmul, pshr;
     long long ps, hs, rs;
 };
 
 inline PagedView paged_view(const PagedDims& d, const sa_paged_cache& c) {
     return PagedView{c.k, c.v, c.table, c.lengths, c.pos, c.seen, d.B, d.Hq, d.Hkv, d.G, d.hu, d.nhb,
-                     d.n_pages, d.page, d.shift, d.max_pages, d.cap, d.ldw, d.ps, d.hs, d.rs};
+                     d.n_pages, d.page, d.max_pages, d.cap, d.ldw, d.pmul, d.pshr, d.ps, d.hs, d.rs};
 }
 
-// Decode: the tiles of all units, in unit order, are split evenly over at
-// most kPgSlots CTAs (on the device, from the lengths there), so a CTA ends
+// Decode: the tiles of all units, in unit order, are split evenly over the
+// resident CTAs (bf16: one of eight warps per SM, fp32: two; on the device, from the lengths there), so a CTA ends
 // at most two units it does not own alone: one record for the unit it
 // continues, one for the unit it begins.
 struct PagedDecodePlan {
     int grid;
     int rec;                               // floats per record: m[hu], l[hu], acc[hu][d]
     int ldx;                               // floats per row of logits
+    int extra;                             // tiles a unit counts more than it has
     size_t off_cnt, off_rec, off_lse, off_x, bytes;
 };
+
+// What a CTA spends on a unit beside its tiles is about the time of 128 KB
+// (48 ragged, windowed sequences: 77 us without, 69 / 63 / 60 / 61 us with
+// 32 / 64 / 128 / 192 KB).
+inline int paged_extra(const PagedDims& d) { return (1 << 17) / (2 * kPgTile * d.d * d.esz()); }
 
 inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
     PagedDecodePlan p;
     const long long tiles = (long long)d.U() * d.nhb * ((d.cap + kPgTile - 1) / kPgTile);
-    p.grid = (int)(tiles < kPgSlots ? tiles : kPgSlots);
+    const int slots = d.bf16 ? kPgSlots / 2 : kPgSlots;
+    p.grid = (int)(tiles < slots ? tiles : slots);
     p.rec = d.hu * (2 + d.d);
+    p.extra = paged_extra(d);
     p.ldx = (d.cap + kPgTile - 1) / kPgTile * kPgTile;
     size_t off = 0;
     p.off_cnt = off; off = align256(off + sizeof(unsigned) * (size_t)d.U() * d.nhb);

@@ -22,16 +22,17 @@ sa_status check_paged_shape(const sa_paged_shape* s, PagedDims* d) {
     d->B = s->B; d->Hq = s->Hq; d->Hkv = s->Hkv; d->G = s->Hq / s->Hkv; d->d = s->d;
     d->bf16 = s->dtype == SA_BF16;
     d->n_pages = s->n_pages; d->page = s->page; d->max_pages = s->max_pages;
-    d->shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (s->page == (1 << i)) d->shift = i;
+    // division of a slot (below 2^30) by the page size as a multiplication:
+    // l = ceil(log2 page), pmul = floor(2^32 (2^l - page) / page) + 1
+    d->pshr = 0;
+    while ((1LL << d->pshr) < s->page) ++d->pshr;
+    d->pmul = (uint32_t)((((1ULL << d->pshr) - (unsigned)s->page) << 32) / (unsigned)s->page + 1);
     d->cap = (int)cap;
     d->ldw = s->ldw == 0 ? d->cap : s->ldw;
     if (d->ldw < d->cap) return SA_ERR_INVALID_ARG;
     // the matrix instructions of the bf16 decode take sixteen rows of queries
     d->hu = d->bf16 && d->G > 8 ? 16 : 8;
     d->nhb = (d->G + d->hu - 1) / d->hu;
-    if ((long long)d->U() * d->nhb * ((d->cap + kPgTile - 1) / kPgTile) >= (1LL << 31)) return SA_ERR_UNSUPPORTED;
     d->ps = s->page_stride; d->hs = s->head_stride; d->rs = s->row_stride;
     if (d->ps == 0 && d->hs == 0 && d->rs == 0) {
         d->rs = s->d;
@@ -41,6 +42,8 @@ sa_status check_paged_shape(const sa_paged_shape* s, PagedDims* d) {
     const int chunk = 16 / d->esz();
     if (d->ps < 1 || d->hs < 1 || d->rs < 1 || d->ps % chunk != 0 || d->hs % chunk != 0 || d->rs % chunk != 0)
         return SA_ERR_INVALID_ARG;
+    if ((long long)d->U() * d->nhb * ((d->cap + kPgTile - 1) / kPgTile + paged_extra(*d)) >= (1LL << 31))
+        return SA_ERR_UNSUPPORTED;
     return SA_OK;
 }
 

@@ -18,23 +18,25 @@ namespace sa {
 #define SA_PG_TILES(io) \
     [&](int b) { return max(1, (pg_list((io).c, b, (io).sink, (io).local).n + kPgTile - 1) / kPgTile); }
 
-// What a CTA needs of the unit its cursor is in.
+// What a CTA needs of the unit its cursor is in: [tile, end) are its tiles, none
+// where its range ends among the extra ones.
 template <typename T, int D>
 struct PgUnit {
     PgList ls;
-    int b, g, nt, end, s1, newest, gh, head0;      // tiles, this CTA's end among them, its last list entry, heads
+    int b, g, nt, tile, end, s1, newest, gh, head0;   // s1: the end of its list entries; gh heads from head0 on
     size_t qh0;
     const T* q;
     const int32_t* trow;
     const int32_t* prow;                           // positions, or null where they are not needed or the slots
-    __device__ __forceinline__ PgUnit(const PgDecodeIo& io, const PgCursor& cur, long long left) {
+    __device__ __forceinline__ PgUnit(const PgDecodeIo& io, const PgSplit& sp, const PgCursor& cur, unsigned left) {
         const PagedView& c = io.c;
         b = cur.b;
         g = cur.sub / c.nhb;
         const int hb = cur.sub - g * c.nhb;
         ls = pg_list(c, b, io.sink, io.local);
         nt = max(1, (ls.n + kPgTile - 1) / kPgTile);
-        end = (int)min((long long)nt, cur.tile + left);
+        tile = max(0, cur.tile - sp.extra);
+        end = max(0, (int)min((unsigned)(nt + sp.extra), cur.tile + left) - sp.extra);
         s1 = min(ls.n, end * kPgTile);
         newest = pg_newest(c, b, ls.len);
         head0 = g * c.G + hb * c.hu;
@@ -56,13 +58,14 @@ template <typename T, int D>
 struct PgPart {
     bool whole;
     float* rec;
-    __device__ __forceinline__ PgPart(const PgDecodeIo& io, const PgCursor& cur, const PgUnit<T, D>& u)
-        : whole(cur.tile == 0 && u.end == u.nt), rec(pg_rec(io.rec, io.c.hu * (2 + D), blockIdx.x, cur.tile == 0)) {}
+    __device__ __forceinline__ PgPart(const PgDecodeIo& io, const PgUnit<T, D>& u)
+        : whole(u.tile == 0 && u.end == u.nt), rec(pg_rec(io.rec, io.c.hu * (2 + D), blockIdx.x, u.tile == 0)) {}
     // accumulator A of dim e of head h, mass L relative to 2^M
     __device__ __forceinline__ void put(const PgDecodeIo& io, const PgUnit<T, D>& u, int h, int e, float A, float M,
                                         float L) const {
         if (whole) {
-            pg_write<D>(io, u.qh0 + h, e, A, M, L);
+            io.out[(u.qh0 + h) * D + e] = A * pg_inv(L);
+            if (e == 0) pg_write_lse(io, u.qh0 + h, M, L);
         } else {
             rec[2 * io.c.hu + h * D + e] = A;
             if (e == 0) { rec[h] = M; rec[io.c.hu + h] = L; }
@@ -75,9 +78,11 @@ template <typename T, int D, int NT>
 __device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgCursor& cur,
                                            const PgUnit<T, D>& u, const PgPart<T, D>& part, float* f) {
     if (part.whole) return;
-    const int first = sp.owner(cur.unit0), n = sp.owner(cur.unit0 + u.nt - 1) - first + 1;
+    const unsigned own0 = cur.unit0 + sp.extra;
+    const int first = (int)sp.owner(own0), n = (int)sp.owner(own0 + u.nt - 1) - first + 1;
     unsigned* cnt = io.cnt + (size_t)cur.b * io.c.Hkv * io.c.nhb + cur.sub;
     if (last_cta_of_unit(cnt, n)) {
+#pragma unroll 1
         for (int h0 = 0; h0 < u.gh; h0 += 8) {
             pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f);
             __syncthreads();
@@ -86,10 +91,18 @@ __device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& 
     }
 }
 
-__device__ __forceinline__ void pg_next(PgCursor& cur, int per, int nt) {
-    cur.unit0 += nt;
+// the cursor's unit that is left, the next one; t0 moves along.  False at the range's end.
+template <typename T, int D>
+__device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp, PgCursor& cur, PgUnit<T, D>& u,
+                                        unsigned& t0, unsigned t1) {
+    const int n = u.nt + sp.extra;
+    t0 += n - cur.tile;                            // past t1 where the unit goes on in another CTA
+    if (t0 >= t1) return false;
+    cur.unit0 += n;
     cur.tile = 0;
-    if (++cur.sub == per) { cur.sub = 0; ++cur.b; }
+    if (++cur.sub == io.c.Hkv * io.c.nhb) { cur.sub = 0; ++cur.b; }
+    u = PgUnit<T, D>(io, sp, cur, t1 - t0);
+    return u.end > u.tile;                         // none of its own: then the range ends there
 }
 
 // ---- bf16: matrix instructions --------------------------------------------------
@@ -106,14 +119,15 @@ __device__ __forceinline__ void pg_next(PgCursor& cur, int per, int nt) {
 // rounding below 32 bits is the cache's own.  With up to four heads rows 4..7
 // repeat rows 0..3 and two of the parts share one instruction.  The maximum is
 // moved only when a logit passes it by 8 (2^8 in the sums): one vote per step.
-constexpr int kPtThreads = 128;
+constexpr int kPtThreads = 256;
 constexpr int kPtWarps = kPtThreads / 32;
+constexpr int kPtStep = kPtWarps * 16;          // list entries of a step of the CTA
 
 template <int D>
 struct PgStage {
     static constexpr int kPitch = 2 * D + 16;
     static constexpr int kBytes = 2 * 16 * kPitch + 16 * 4;      // K rows, V rows, distances
-    static constexpr int kStages = D == 128 ? 3 : 5;             // with the scratch, what two CTAs per SM have room for
+    static constexpr int kStages = D == 128 ? 3 : 5;             // with the scratch, what an SM has room for
     static constexpr int kRing = kPtWarps * kStages * kBytes;
     static constexpr int kAcc = kPtWarps * 4 * (D + 4);          // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
@@ -133,7 +147,7 @@ __device__ __forceinline__ void split3(float p0, float p1, uint32_t& hi, uint32_
 }
 
 template <int D, int HB>
-__global__ void __launch_bounds__(kPtThreads, 2)
+__global__ void __launch_bounds__(kPtThreads, 1)
 k_paged_tc(PgDecodeIo io) {
     using T = __nv_bfloat16;
     using St = PgStage<D>;
@@ -154,19 +168,21 @@ k_paged_tc(PgDecodeIo io) {
     const T* V = static_cast<const T*>(c.v) + (lane % CPR) * 8;
     PgSplit sp;
     PgCursor cur;
-    long long t0, t1;
+    unsigned t0, t1;
     cudaTriggerProgrammaticLaunchCompletion();                   // the weights' kernel may come and wait
-    if (!pg_locate<kPtThreads>(c.B, per, io.min_tiles, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
+    if (!pg_locate<kPtThreads>(c.B, per, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
     int head[R], stage = 0;                                       // ring stage of the unit's first step
     uint32_t qa[KS][2 * R];
     float sl[R];
     PgRaw ahead;
-    PgUnit<T, D> u(io, cur, t1 - t0);
-    int row0, n;                                                  // this warp's steps: 16 list entries from row0 + i kPgTile
+    int row0, n = 0;                                              // this warp's steps: 16 list entries from row0 + i kPtStep
+    PgUnit<T, D> u(io, sp, cur, t1 - t0), done = u;               // the unit at hand, the one before it
+    PgCursor at = cur;                                            // of `done`
+    float m[R], l[R], o[R][MT][4];                                // maxima, masses, accumulators of the unit
 
     auto fetch = [&](int i) {
-        return pg_fetch(io, u.ls, u.trow, u.prow, row0 + i * kPgTile + (lane & 15), i < n ? u.s1 : 0);
+        return pg_fetch(io, u.ls, u.trow, u.prow, row0 + i * kPtStep + (lane & 15), i < n ? u.s1 : 0);
     };
     auto issue = [&](int i, const PgRaw& raw) {
         float dist;
@@ -185,8 +201,9 @@ k_paged_tc(PgDecodeIo io) {
     // a unit's queries and the copies of its first steps; runs while the unit
     // before it is handed in
     auto begin = [&]() {
-        row0 = cur.tile * kPgTile + warp * 16;
-        n = u.s1 > row0 ? (u.s1 - row0 + kPgTile - 1) / kPgTile : 0;
+        stage = (stage + n) % S;
+        row0 = u.tile * kPgTile + warp * 16;
+        n = u.s1 > row0 ? (u.s1 - row0 + kPtStep - 1) / kPtStep : 0;
         PgRaw raw[S - 1];
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) raw[i] = fetch(i);
@@ -208,10 +225,54 @@ k_paged_tc(PgDecodeIo io) {
         }
         ahead = fetch(S - 1);
     };
-    begin();
-
-    for (;;) {
-        float m[R], l[R], o[R][MT][4];
+#pragma unroll 1
+    for (bool handed = true, more = u.end > u.tile;;) {
+        if (more) begin();
+        if (!handed) {
+            const PgPart<T, D> part(io, done);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                if (t == 0 && (HB != 4 || r < 4)) {
+                    s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][0] = m[k];
+                    s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][1] = l[k];
+                }
+            }
+            // four heads at a time through the scratch
+#pragma unroll
+            for (int hq = 0; hq < HB / 4; ++hq) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float y = o[hq / 2][mt][j];
+                        if (HB == 4) y += __shfl_xor_sync(0xffffffffu, y, 2);        // its parts' two columns
+                        if (t / 2 == (hq & 1))
+                            scratch[(warp * 4 + (2 * t + (j & 1)) % 4) * LD + mt * 16 + r + (j >> 1) * 8] = y;
+                    }
+                __syncthreads();
+                for (int x = threadIdx.x; x < 4 * D; x += kPtThreads) {
+                    const int h4 = x / D, e = x - h4 * D, h = 4 * hq + h4;
+                    if (h >= done.gh) break;
+                    float M = -INFINITY, A = 0.f, L = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kPtWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
+#pragma unroll
+                    for (int w = 0; w < kPtWarps; ++w) {
+                        const float mw = s_ml[w][h][0];
+                        const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+                        A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
+                        L = fmaf(s_ml[w][h][1], f, L);
+                    }
+                    part.put(io, done, h, e, A, M, L);
+                }
+                __syncthreads();
+            }
+            pg_hand_in<T, D, kPtThreads>(io, sp, at, done, part, scratch);
+        }
+        if (!more) break;
+        __syncthreads();                                          // the scratch has been read
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             m[k] = -INFINITY;
@@ -221,6 +282,7 @@ k_paged_tc(PgDecodeIo io) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[k][mt][j] = 0.f;
         }
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             __syncwarp();                                         // stage i - 1 has been read by all lanes
             if (i + S - 1 < n) issue(i + S - 1, ahead);
@@ -262,7 +324,7 @@ k_paged_tc(PgDecodeIo io) {
                     rises |= x[k][j] > m[k] + 8.f;
                 }
             if (io.x != nullptr) {
-                const int y = row0 + i * kPgTile + 2 * t;
+                const int y = row0 + i * kPtStep + 2 * t;
 #pragma unroll
                 for (int k = 0; k < R; ++k)
                     if (head[k] < u.gh && (HB != 4 || r < 4)) {
@@ -320,59 +382,10 @@ k_paged_tc(PgDecodeIo io) {
         }
         __syncwarp();
         // the unit is done: its successor's first copies go out before it is handed in
-        const PgUnit<T, D> done = u;
-        const PgCursor at = cur;
-        t0 += u.end - cur.tile;
-        const bool more = t0 < t1;
-        stage = (stage + n) % S;
-        if (more) {
-            pg_next(cur, per, u.nt);
-            u = PgUnit<T, D>(io, cur, t1 - t0);
-            begin();
-        }
-        const PgPart<T, D> part(io, at, done);
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-            l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-            if (t == 0 && (HB != 4 || r < 4)) {
-                s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][0] = m[k];
-                s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][1] = l[k];
-            }
-        }
-        // four heads at a time through the scratch
-#pragma unroll
-        for (int hq = 0; hq < HB / 4; ++hq) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float y = o[hq / 2][mt][j];
-                    if (HB == 4) y += __shfl_xor_sync(0xffffffffu, y, 2);        // its parts' two columns
-                    if (t / 2 == (hq & 1))
-                        scratch[(warp * 4 + (2 * t + (j & 1)) % 4) * LD + mt * 16 + r + (j >> 1) * 8] = y;
-                }
-            __syncthreads();
-            for (int x = threadIdx.x; x < 4 * D; x += kPtThreads) {
-                const int h4 = x / D, e = x - h4 * D, h = 4 * hq + h4;
-                if (h >= done.gh) break;
-                float M = -INFINITY, A = 0.f, L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kPtWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
-#pragma unroll
-                for (int w = 0; w < kPtWarps; ++w) {
-                    const float mw = s_ml[w][h][0];
-                    const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-                    A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
-                    L = fmaf(s_ml[w][h][1], f, L);
-                }
-                part.put(io, done, h, e, A, M, L);
-            }
-            __syncthreads();
-        }
-        pg_hand_in<T, D, kPtThreads>(io, sp, at, done, part, scratch);
-        if (!more) break;
-        __syncthreads();
+        done = u;
+        at = cur;
+        handed = false;
+        more = pg_next(io, sp, cur, u, t0, t1);
     }
     tc::cp_wait<0>();
 }
@@ -396,12 +409,13 @@ k_paged_cc(PgDecodeIo io) {
     const int per = c.Hkv * c.nhb;
     PgSplit sp;
     PgCursor cur;
-    long long t0, t1;
+    unsigned t0, t1;
     cudaTriggerProgrammaticLaunchCompletion();
-    if (!pg_locate<kThreads>(c.B, per, io.min_tiles, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
+    if (!pg_locate<kThreads>(c.B, per, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
-    while (t0 < t1) {
-        const PgUnit<T, D> u(io, cur, t1 - t0);
+    PgUnit<T, D> u(io, sp, cur, t1 - t0);
+#pragma unroll 1
+    for (bool more = u.end > u.tile; more;) {
         const T* K = static_cast<const T*>(c.k) + li * EPC;
         const T* V = static_cast<const T*>(c.v) + li * EPC;
         float qv[GB][EPC], sl[GB];
@@ -417,7 +431,7 @@ k_paged_cc(PgDecodeIo io) {
         }
         Online<GB, EPC> os;
         os.init();
-        for (int wt = cur.tile * kPgTile + warp * UN * GPW; wt < u.s1; wt += UN * NG) {
+        for (int wt = u.tile * kPgTile + warp * UN * GPW; wt < u.s1; wt += UN * NG) {
             uint4 wk[UN], wv[UN];
             float dist[UN];
             bool ok[UN];
@@ -449,15 +463,14 @@ k_paged_cc(PgDecodeIo io) {
         }
         warp_merge<GB, EPC, CPR>(os);
         cta_merge_store<GB, EPC, CPR, D>(os, sm, s_own);         // m[GB], l[GB], acc[GB][D]
-        const PgPart<T, D> part(io, cur, u);
+        const PgPart<T, D> part(io, u);
         for (int x = threadIdx.x; x < u.gh * D; x += kThreads) {
             const int h = x / D, e = x - h * D;
             part.put(io, u, h, e, s_own[2 * GB + x], s_own[h], s_own[GB + h]);
         }
         pg_hand_in<T, D, kThreads>(io, sp, cur, u, part, s_join);
         __syncthreads();
-        t0 += u.end - cur.tile;
-        pg_next(cur, per, u.nt);
+        more = pg_next(io, sp, cur, u, t0, t1);
     }
 }
 
@@ -474,11 +487,11 @@ k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
     auto tiles = [&](int b) { return max(1, (pg_length(c, b) + kPgWTile - 1) / kPgWTile); };
     PgSplit sp;
     PgCursor cur;
-    long long t0, t1;
-    const bool any = pg_locate<kThreads>(c.B, c.Hkv, 1, blockIdx.x, tiles, sp, cur, t0, t1);
+    unsigned t0, t1;
+    const bool any = pg_locate<kThreads>(c.B, c.Hkv, 0, blockIdx.x, tiles, sp, cur, t0, t1);
     cudaGridDependencySynchronize();               // the logits and masses
     if (!any) return;
-    for (long long t = t0; t < t1; ++t) {
+    for (unsigned t = t0; t < t1; ++t) {
         const int b = cur.b, g = cur.sub;
         const PgList ls = pg_list(c, b, io.sink, io.local);
         const size_t u = (size_t)b * c.Hkv + g, row = u * c.ldw;
@@ -564,8 +577,8 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     io.cap_out = a.softcap * kLog2e;
     io.sink = a.sink;
     io.local = a.local;
-    io.min_tiles = 1;
     io.ldx = p.ldx;
+    io.extra = p.extra;
     const cudaError_t e = d.d == 128 ? decode_launch<128>(d, p, io, s) : decode_launch<64>(d, p, io, s);
     if (e != cudaSuccess || !weights) return e;
     const long long steps = (long long)d.U() * ((d.cap + kPgWTile - 1) / kPgWTile);

@@ -20,7 +20,7 @@ struct PgDecodeIo {
     unsigned* cnt;           // completion tickets, one per unit
     float scale, qscale;     // softmax scale, and times log2(e)
     float softcap, cap_in, cap_out;    // c, scale / c, c log2(e)
-    int sink, local, min_tiles, ldx;
+    int sink, local, ldx, extra;
 };
 
 // logit in log2 units: the dot product scaled, capped (tanhf: 2 ulp, so that
@@ -64,28 +64,27 @@ __device__ __forceinline__ float* pg_rec(float* rec, int floats, int cta, bool b
     return rec + (size_t)(2 * cta + (begins ? 1 : 0)) * floats;
 }
 
-// one row's outputs: accumulator A of dim e, mass L relative to 2^M
-template <int D>
-__device__ __forceinline__ void pg_write(const PgDecodeIo& io, size_t qh, int e, float A, float M, float L) {
-    io.out[qh * D + e] = L == 0.f ? 0.f : A / L;
-    if (e == 0) {
-        const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
-        if (io.lse != nullptr) io.lse[qh] = l2 * kLn2;
-        if (io.x != nullptr) io.lse2[qh] = l2;
-    }
+// a head's log of its mass L 2^M
+__device__ __forceinline__ void pg_write_lse(const PgDecodeIo& io, size_t qh, float M, float L) {
+    const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
+    if (io.lse != nullptr) io.lse[qh] = l2 * kLn2;
+    if (io.x != nullptr) io.lse2[qh] = l2;
 }
+
+// 1 / L, and 0 where nothing is seen (out = A inv: one rounding more than A / L)
+__device__ __forceinline__ float pg_inv(float L) { return L == 0.f ? 0.f : 1.f / L; }
 
 // The unit's last CTA joins its n records (fixed order) and writes the rows of
 // its gh <= 8 heads from h0 on.  Thread (column, part): a column is four dims of
 // a head, and the records are cut into as many parts as there are threads for;
 // a part's first records are on their way before the weights are known.
 // f: shared scratch of kPgJoinFloats floats.  All threads call.
-constexpr int kPgJoin = 12;                // records of a part in flight
+constexpr int kPgJoin = 10;                // records of a part in flight
 // the heads' m and l, then [head][record] weights, then over them the parts' sums (a float4 per thread)
 constexpr int kPgJoinFloats = 8 * (kPgSlots + 2);
 
 template <int D, int NT>
-__device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
+__device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
     const int hu = io.c.hu, floats = hu * (2 + D);
     float* sM = f;
     float* sL = f + 8;
@@ -93,59 +92,70 @@ __device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int 
     float4* sums = reinterpret_cast<float4*>(w);
     static_assert(16 + 4 * NT <= kPgJoinFloats, "the parts' sums lie over the weights");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto rec = [&](int s) -> const float* { return pg_rec(io.rec, floats, first + s, s == 0) + h0; };
+    const float* rest = pg_rec(io.rec, floats, first, false) + h0;         // record s > 0: 2 s records on
+    const float* begin = pg_rec(io.rec, floats, first, true) + h0;
+    auto rec = [&](int s) { return s == 0 ? begin : rest + (size_t)(2 * s) * floats; };
     const int cols = gh * (D / 4);
-    const int parts = max(1, NT / cols);
-    const int part = threadIdx.x / cols;       // >= parts: none
+    const int parts = max(1, NT / cols), part = threadIdx.x / cols;        // part >= parts: none
     const int each = (n + parts - 1) / parts;
+#pragma unroll 1
+    for (int x = warp; x < gh; x += NT / 32) {
+        // the first 32 records' m and l at once
+        float m = lane < n ? __ldcg(rec(lane) + x) : -INFINITY, l = lane < n ? __ldcg(rec(lane) + hu + x) : 0.f;
+        float M = m;
+#pragma unroll 1
+        for (int s = lane; s < n;) {
+            w[x * n + s] = m;
+            s += 32;
+            if (s < n) {
+                m = __ldcg(rec(s) + x);
+                M = (m > M || m != m) ? m : M; // NaN stays
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, M, o);
+            M = (y > M || y != y) ? y : M;
+        }
+        float L = 0.f;
+#pragma unroll 1
+        for (int s = lane; s < n;) {
+            const float q = w[x * n + s], y = q == -INFINITY ? 0.f : ex2(q - M);
+            w[x * n + s] = y;
+            L = fmaf(l, y, L);
+            s += 32;
+            if (s < n) l = __ldcg(rec(s) + hu + x);
+        }
+        L = group_sum<32>(L);
+        if (lane == 0) {
+            sM[x] = M;
+            sL[x] = pg_inv(L);
+            pg_write_lse(io, qh0 + x, M, L);
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int c0 = 0; c0 < cols; c0 += NT) {
-        const int col = c0 + (parts > 1 ? threadIdx.x % cols : threadIdx.x);
+        const int col = parts > 1 ? threadIdx.x % cols : c0 + threadIdx.x;
         const int h = col / (D / 4), e = (col % (D / 4)) * 4;
         const int s0 = parts > 1 ? part * each : 0, s1 = min(n, s0 + each);
         const bool mine = col < cols && (parts == 1 || part < parts);
-        float4 a[kPgJoin];
-        auto load = [&](int s) {
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int s = s0; mine && s < s1; s += kPgJoin) {
+            float4 a[kPgJoin];
 #pragma unroll
             for (int j = 0; j < kPgJoin; ++j)
-                a[j] = mine && s + j < s1 ? __ldcg(reinterpret_cast<const float4*>(rec(s + j) - h0 + 2 * hu + (h0 + h) * D + e))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        load(s0);
-        if (c0 == 0) {
-            for (int x = warp; x < gh; x += NT / 32) {
-                float M = -INFINITY;
-                for (int s = lane; s < n; s += 32) {
-                    const float m = __ldcg(rec(s) + x);
-                    w[x * n + s] = m;
-                    M = (m > M || m != m) ? m : M;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const float y = __shfl_xor_sync(0xffffffffu, M, o);
-                    M = (y > M || y != y) ? y : M;
-                }
-                float L = 0.f;
-                for (int s = lane; s < n; s += 32) {
-                    const float m = w[x * n + s];
-                    const float y = m == -INFINITY ? 0.f : ex2(m - M);
-                    w[x * n + s] = y;
-                    L = fmaf(__ldcg(rec(s) + hu + x), y, L);
-                }
-                L = group_sum<32>(L);
-                if (lane == 0) { sM[x] = M; sL[x] = L; }
-            }
-            __syncthreads();
-        }
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = s0; mine && s < s1; s += kPgJoin) {
-            if (s > s0) load(s);
+                if (s + j < s1) a[j] = __ldcg(reinterpret_cast<const float4*>(rec(s + j) - h0 + 2 * hu + (h0 + h) * D + e));
 #pragma unroll
             for (int j = 0; j < kPgJoin; ++j) {
-                const float y = s + j < s1 ? w[h * n + s + j] : 0.f;
-                A.x = fmaf(a[j].x, y, A.x);
-                A.y = fmaf(a[j].y, y, A.y);
-                A.z = fmaf(a[j].z, y, A.z);
-                A.w = fmaf(a[j].w, y, A.w);
+                if (s + j < s1) {
+                    const float y = w[h * n + s + j];
+                    A.x = fmaf(a[j].x, y, A.x);
+                    A.y = fmaf(a[j].y, y, A.y);
+                    A.z = fmaf(a[j].z, y, A.z);
+                    A.w = fmaf(a[j].w, y, A.w);
+                }
             }
         }
         if (parts > 1) {
@@ -158,11 +168,8 @@ __device__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int 
             }
         }
         if (mine && (parts == 1 || part == 0)) {
-            const float M = sM[h], L = sL[h];
-            pg_write<D>(io, qh0 + h, e, A.x, M, L);
-            pg_write<D>(io, qh0 + h, e + 1, A.y, M, L);
-            pg_write<D>(io, qh0 + h, e + 2, A.z, M, L);
-            pg_write<D>(io, qh0 + h, e + 3, A.w, M, L);
+            const float inv = sL[h];
+            *reinterpret_cast<float4*>(io.out + (qh0 + h) * D + e) = make_float4(A.x * inv, A.y * inv, A.z * inv, A.w * inv);
         }
     }
 }
