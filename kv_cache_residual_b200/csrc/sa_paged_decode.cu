@@ -391,21 +391,32 @@ k_paged_tc(PgDecodeIo io) {
 }
 
 // ---- fp32: CUDA cores --------------------------------------------------------------
-// A lane group reads one cache row per step (16-byte loads, four rows in
-// flight) and keeps the unit's states in registers.
+// A lane group reads UN cache rows at a time (16-byte loads; the table a step
+// ahead).  Their UN GB dot products are summed across the group's W lanes by
+// halves, so that they end spread over the lanes: a lane caps, masks and
+// exponentiates its own, and the weights come back by shuffles.
+template <int GB>
+struct PgCc {
+    static constexpr int UN = GB == 8 ? 2 : 4;
+};
+
 template <int D, int GB>
 __global__ void __launch_bounds__(kThreads, 2)
 k_paged_cc(PgDecodeIo io) {
     using T = float;
     using Gm = Geom<T, D>;
-    constexpr int EPC = Gm::EPC, CPR = Gm::CPR, GPW = Gm::GPW, NG = Gm::NG;
-    constexpr int UN = 4;                      // rows in flight per lane group
+    constexpr int EPC = Gm::EPC, W = Gm::CPR, GPW = Gm::GPW, NG = Gm::NG, UN = PgCc<GB>::UN;
+    // dot product x = row GB + head: the lanes x DUP / NPL .. of the group, their register x % NPL
+    constexpr int NV = UN * GB, NPL = NV > W ? NV / W : 1, DUP = NV < W ? W / NV : 1;
+    constexpr int JS = GB * DUP / NPL;         // lanes from a row to the next
+    static_assert(JS >= 1, "a lane's dot products are of one row");
     __shared__ float sm[kWarps * GB * (D + 2)];
     __shared__ float s_own[GB * (D + 2)];
     __shared__ __align__(16) float s_join[kPgJoinFloats];
     const PagedView& c = io.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int li = lane % CPR, gsub = lane / CPR;
+    const int li = lane % W, gsub = lane / W, lane0 = lane - li;
+    const int row = li / JS, head0 = li * NPL / DUP % GB;      // of this lane's dot products
     const int per = c.Hkv * c.nhb;
     PgSplit sp;
     PgCursor cur;
@@ -418,10 +429,14 @@ k_paged_cc(PgDecodeIo io) {
     for (bool more = u.end > u.tile; more;) {
         const T* K = static_cast<const T*>(c.k) + li * EPC;
         const T* V = static_cast<const T*>(c.v) + li * EPC;
-        float qv[GB][EPC], sl[GB];
+        const bool own_pos = u.prow != nullptr;
+        float qv[GB][EPC], sl[NPL];
+        PgRaw raw[UN];
+        int wt = u.tile * kPgTile + warp * UN * GPW;
+#pragma unroll
+        for (int j = 0; j < UN; ++j) raw[j] = pg_fetch(io, u.ls, u.trow, u.prow, wt + j * GPW + gsub, u.s1);
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
-            sl[h] = u.slope2(io, h);
             if (h < u.gh) {
                 unpack<T>(ld_nc16(u.q + (size_t)h * D + li * EPC), qv[h]);
             } else {
@@ -429,40 +444,114 @@ k_paged_cc(PgDecodeIo io) {
                 for (int e = 0; e < EPC; ++e) qv[h][e] = 0.f;
             }
         }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) sl[i] = u.slope2(io, head0 + i);
+        float m[NPL], l[NPL];
         Online<GB, EPC> os;
         os.init();
-        for (int wt = u.tile * kPgTile + warp * UN * GPW; wt < u.s1; wt += UN * NG) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+#pragma unroll 1
+        for (; wt < u.s1; wt += UN * NG) {
             uint4 wk[UN], wv[UN];
-            float dist[UN];
-            bool ok[UN];
+            float dist = 0.f;
+            bool seen = false;                                 // of this lane's row
 #pragma unroll
             for (int j = 0; j < UN; ++j) {
-                const PgRaw raw = pg_fetch(io, u.ls, u.trow, u.prow, wt + j * GPW + gsub, u.s1);
-                const long long off = pg_see(io, raw, u.prow != nullptr, u.g, u.newest, dist[j]);
-                ok[j] = off >= 0;
-                wk[j] = ok[j] ? ld_stream16(K + off) : make_uint4(0, 0, 0, 0);
-                wv[j] = ok[j] ? ld_stream16(V + off) : make_uint4(0, 0, 0, 0);
+                float dj;
+                const long long off = pg_see(io, raw[j], own_pos, u.g, u.newest, dj);
+                wk[j] = off >= 0 ? ld_stream16(K + off) : make_uint4(0, 0, 0, 0);
+                wv[j] = off >= 0 ? ld_stream16(V + off) : make_uint4(0, 0, 0, 0);
+                if (row == j) { dist = dj; seen = off >= 0; }
             }
+            const int y = wt + row * GPW + gsub;
+#pragma unroll
+            for (int j = 0; j < UN; ++j)
+                raw[j] = pg_fetch(io, u.ls, u.trow, u.prow, wt + UN * NG + j * GPW + gsub, u.s1);
+            float v[NV];
 #pragma unroll
             for (int j = 0; j < UN; ++j) {
-                const int y = wt + j * GPW + gsub;
-                float kf[EPC], vf[EPC];
+                float kf[EPC];
                 unpack<T>(wk[j], kf);
-                unpack<T>(wv[j], vf);
 #pragma unroll
                 for (int h = 0; h < GB; ++h) {
                     float x = 0.f;
 #pragma unroll
                     for (int e = 0; e < EPC; ++e) x = fmaf(qv[h][e], kf[e], x);
-                    x = pg_logit(io, group_sum<CPR>(x), sl[h], dist[j]);
-                    if (ok[j] && x != -INFINITY) os.add(h, x, vf);       // e^-inf: no weight
-                    if (io.x != nullptr && li == h % CPR && h < u.gh && y < u.s1)
-                        io.x[(u.qh0 + h) * io.ldx + y] = ok[j] ? x : -INFINITY;
+                    v[j * GB + h] = x;
+                }
+            }
+            // sums over the group's lanes: while a lane has several, it gives half away
+#pragma unroll
+            for (int off = W / 2, n = NV; off > 0; off >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+                    const bool up = (li & off) != 0;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float give = up ? v[i] : v[i + n];
+                        v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                } else {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+                }
+            }
+            bool rises = false;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                v[i] = seen ? pg_logit(io, v[i], sl[i], dist) : -INFINITY;
+                rises |= v[i] > m[i] + 8.f;
+                if (io.x != nullptr && li % DUP == 0 && head0 + i < u.gh && y < u.s1)
+                    io.x[(u.qh0 + head0 + i) * io.ldx + y] = v[i];
+            }
+            if (__any_sync(0xffffffffu, rises)) {
+                float sc[NPL];
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    float mx = fmaxf(m[i], v[i]);
+#pragma unroll
+                    for (int off = JS; off < W; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    sc[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx);
+                    l[i] *= sc[i];
+                    m[i] = mx;
+                }
+#pragma unroll
+                for (int h = 0; h < GB; ++h) {
+                    const float f = __shfl_sync(0xffffffffu, sc[h % NPL], lane0 + h * DUP / NPL);
+#pragma unroll
+                    for (int e = 0; e < EPC; ++e) os.acc[h][e] *= f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                v[i] = v[i] == -INFINITY ? 0.f : ex2(v[i] - m[i]);         // e^-inf: no weight
+                l[i] += v[i];
+            }
+#pragma unroll
+            for (int j = 0; j < UN; ++j) {
+                float vf[EPC];
+                unpack<T>(wv[j], vf);
+#pragma unroll
+                for (int h = 0; h < GB; ++h) {
+                    const int x = j * GB + h;
+                    const float p = __shfl_sync(0xffffffffu, v[x % NPL], lane0 + x * DUP / NPL);
+#pragma unroll
+                    for (int e = 0; e < EPC; ++e) os.acc[h][e] = fmaf(p, vf[e], os.acc[h][e]);
                 }
             }
         }
-        warp_merge<GB, EPC, CPR>(os);
-        cta_merge_store<GB, EPC, CPR, D>(os, sm, s_own);         // m[GB], l[GB], acc[GB][D]
+        // the rows' sums, then every head's state in every lane of the group
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+#pragma unroll
+            for (int off = JS; off < W; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+#pragma unroll
+        for (int h = 0; h < GB; ++h) {
+            os.m[h] = __shfl_sync(0xffffffffu, m[h % NPL], lane0 + h * DUP / NPL);
+            os.l[h] = __shfl_sync(0xffffffffu, l[h % NPL], lane0 + h * DUP / NPL);
+        }
+        warp_merge<GB, EPC, W>(os);
+        cta_merge_store<GB, EPC, W, D>(os, sm, s_own);         // m[GB], l[GB], acc[GB][D]
         const PgPart<T, D> part(io, u);
         for (int x = threadIdx.x; x < u.gh * D; x += kThreads) {
             const int h = x / D, e = x - h * D;
