@@ -11,7 +11,7 @@
 namespace sa {
 
 constexpr int kPgTile = 64;            // slots per tile: the unit of the split over a cache's length
-constexpr int kPgSlots = 148 * 2;      // most CTAs of the decode
+constexpr int kPgSlots = 148;          // CTAs of the decode: one per SM
 
 struct PagedDims {
     int B, Hq, Hkv, G, d;
@@ -44,8 +44,8 @@ inline PagedView paged_view(const PagedDims& d, const sa_paged_cache& c) {
                      d.n_pages, d.page, d.max_pages, d.cap, d.ldw, d.pmul, d.pshr, d.ps, d.hs, d.rs};
 }
 
-// Decode: the tiles of all units, in unit order, are split evenly over the
-// resident CTAs (bf16: one of eight warps per SM, fp32: two; on the device, from the lengths there), so a CTA ends
+// Decode: the tiles of all units, in unit order, are split evenly over at
+// most kPgSlots CTAs (on the device, from the lengths there), so a CTA ends
 // at most two units it does not own alone: one record for the unit it
 // continues, one for the unit it begins.
 struct PagedDecodePlan {
@@ -64,8 +64,7 @@ inline int paged_extra(const PagedDims& d) { return (1 << 17) / (2 * kPgTile * d
 inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
     PagedDecodePlan p;
     const long long tiles = (long long)d.U() * d.nhb * ((d.cap + kPgTile - 1) / kPgTile);
-    const int slots = d.bf16 ? kPgSlots / 2 : kPgSlots;
-    p.grid = (int)(tiles < slots ? tiles : slots);
+    p.grid = (int)(tiles < kPgSlots ? tiles : kPgSlots);
     p.rec = d.hu * (2 + d.d);
     p.extra = paged_extra(d);
     p.ldx = (d.cap + kPgTile - 1) / kPgTile * kPgTile;

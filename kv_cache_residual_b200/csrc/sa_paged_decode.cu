@@ -3,12 +3,12 @@
 //   x_hs = cap(scale q_h . k_s) - slope_h (newest - pos_s)
 //   out_h = sum_s softmax_s(x_hs) v_s          (one pass, running maximum and sum)
 //
-// A unit is a KV head of a sequence with up to eight of its query heads.  All
-// units' 64-slot tiles are split evenly over two CTAs per SM (sa_paged.cuh), so
-// ragged batches, one long sequence and many short ones load the GPU alike; a
-// unit cut by the split is joined by the last of its CTAs to finish.
-//
-// k_paged_tc (bf16): matrix instructions.  k_paged_cc (fp32): CUDA cores.
+// A unit is a KV head of a sequence with up to eight (bf16: sixteen) of its
+// query heads.  All units' 64-slot tiles are split evenly over one CTA per SM
+// (sa_paged.cuh), so ragged batches, one long sequence and many short ones load
+// the GPU alike; a unit cut by the split is joined by the last of its CTAs to
+// finish.  Bound: HBM for the rows; for few of them the chain lengths, table,
+// rows, record, ticket, join.
 #include "sa_paged_decode.cuh"
 #include "sa_tc.cuh"
 
@@ -24,6 +24,8 @@ template <typename T, int D>
 struct PgUnit {
     PgList ls;
     int b, g, nt, tile, end, s1, newest, gh, head0;   // s1: the end of its list entries; gh heads from head0 on
+    int index;                                     // of the unit, and of its first own tile
+    unsigned own0;
     size_t qh0;
     const T* q;
     const int32_t* trow;
@@ -41,12 +43,15 @@ struct PgUnit {
         newest = pg_newest(c, b, ls.len);
         head0 = g * c.G + hb * c.hu;
         gh = min(c.hu, c.G - hb * c.hu);
+        index = b * c.Hkv * c.nhb + cur.sub;
+        own0 = cur.unit0 + sp.extra;
         qh0 = (size_t)b * c.Hq + head0;
         q = static_cast<const T*>(io.q) + (long long)b * io.q_stride + (long long)head0 * D;
         trow = c.table + (size_t)b * c.max_pages;
         prow = c.pos == nullptr || (io.local == 0 && io.slopes == nullptr)
                    ? nullptr : c.pos + ((size_t)b * c.Hkv + g) * c.ldw;
     }
+    __device__ __forceinline__ bool any() const { return end > tile; }
     __device__ __forceinline__ float slope2(const PgDecodeIo& io, int h) const {
         return h < gh && io.slopes != nullptr ? __ldg(io.slopes + head0 + h) * kLog2e : 0.f;
     }
@@ -75,12 +80,11 @@ struct PgPart {
 
 // after all have put: the unit's last CTA joins.  All threads call; f as pg_join.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgCursor& cur,
-                                           const PgUnit<T, D>& u, const PgPart<T, D>& part, float* f) {
+__device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgUnit<T, D>& u,
+                                           const PgPart<T, D>& part, float* f) {
     if (part.whole) return;
-    const unsigned own0 = cur.unit0 + sp.extra;
-    const int first = (int)sp.owner(own0), n = (int)sp.owner(own0 + u.nt - 1) - first + 1;
-    unsigned* cnt = io.cnt + (size_t)cur.b * io.c.Hkv * io.c.nhb + cur.sub;
+    const int first = (int)sp.owner(u.own0), n = (int)sp.owner(u.own0 + u.nt - 1) - first + 1;
+    unsigned* cnt = io.cnt + u.index;
     if (last_cta_of_unit(cnt, n)) {
 #pragma unroll 1
         for (int h0 = 0; h0 < u.gh; h0 += 8) {
@@ -91,45 +95,50 @@ __device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& 
     }
 }
 
-// the cursor's unit that is left, the next one; t0 moves along.  False at the range's end.
-template <typename T, int D>
-__device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp, PgCursor& cur, PgUnit<T, D>& u,
-                                        unsigned& t0, unsigned t1) {
-    const int n = u.nt + sp.extra;
+// Moves the cursor from its unit, nt tiles long, to the next; t0 moves along.
+// False at the range's end.
+__device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp, PgCursor& cur, int nt, unsigned& t0,
+                                        unsigned t1) {
+    const int n = nt + sp.extra;
     t0 += n - cur.tile;                            // past t1 where the unit goes on in another CTA
     if (t0 >= t1) return false;
     cur.unit0 += n;
     cur.tile = 0;
     if (++cur.sub == io.c.Hkv * io.c.nhb) { cur.sub = 0; ++cur.b; }
-    u = PgUnit<T, D>(io, sp, cur, t1 - t0);
-    return u.end > u.tile;                         // none of its own: then the range ends there
+    return true;
 }
 
-// ---- bf16: matrix instructions --------------------------------------------------
-// A warp takes 16 of a tile's slots through a ring of its own (cp.async, rows
-// padded by 16 bytes for ldmatrix), with no barrier among warps until the unit
-// ends:
-//   S   = Q K^T     A = the unit's queries, B = 16 key rows (ldmatrix)
-//   O^T += V^T P^T  A = value rows (ldmatrix.trans), B = the weights: the layout
-//                   of S's accumulators is that of B's fragments, so weights
-//                   never move between lanes
+// ---- the pass --------------------------------------------------------------------
+// A warp takes 16 slots of a step through a ring of its own (cp.async, padded
+// rows), with no barrier among warps until the unit ends:
+//   S   = Q K^T     A = the unit's queries, B = 16 key rows
+//   O^T += V^T P^T  A = value rows, B = the weights: the layout of S's
+//                   accumulators is that of B's fragments, so weights never
+//                   move between lanes
 // Lane (r = lane / 4, t = lane % 4) holds row r (and r + 8 where HB = 16) of S at
-// slots 2t, 2t+1, 8+2t, 9+2t, and dims 16 i + r, + 8 of heads 2t, 2t+1 of O^T.
-// Weights are fp32: they enter as three bf16 parts (24 bits), so that the only
-// rounding below 32 bits is the cache's own.  With up to four heads rows 4..7
-// repeat rows 0..3 and two of the parts share one instruction.  The maximum is
-// moved only when a logit passes it by 8 (2^8 in the sums): one vote per step.
-constexpr int kPtThreads = 256;
-constexpr int kPtWarps = kPtThreads / 32;
-constexpr int kPtStep = kPtWarps * 16;          // list entries of a step of the CTA
-
-template <int D>
-struct PgStage {
-    static constexpr int kPitch = 2 * D + 16;
-    static constexpr int kBytes = 2 * 16 * kPitch + 16 * 4;      // K rows, V rows, distances
+// slots 2t, 2t+1, 8+2t, 9+2t, and of O^T 2 MT dims of heads 2t, 2t+1.
+//
+// What is fp32 enters as three bf16 parts of 8 bits each, cut off the top, so
+// that nothing is rounded on the way in: the weights always, and with fp32
+// caches queries, keys and values too, of whose nine products of parts all that
+// reach 2^-24 of the whole are taken.  (m16n8k16 with bf16 rows leaves the
+// tensor pipe under a fifth busy at HBM speed, the parts of fp32 rows under a
+// half; tcgen05 would want the eight query rows padded to 64 or 128.)  With up
+// to four heads rows 4..7 repeat rows 0..3 and two of the weights' parts share
+// one instruction.  The maximum is moved only when a logit passes it by 8 (2^8
+// in the sums): one vote per step.
+template <typename T, int D>
+struct PgTc {
+    static constexpr bool kBf16 = sizeof(T) == 2;
+    static constexpr int kWarps = kBf16 ? 8 : 4, kThreads = kWarps * 32;
+    static constexpr int kStep = kWarps * 16;                    // list entries of a step of the CTA
+    // row pitches without bank conflicts: bf16, ldmatrix; fp32, a lane's four
+    // dims of row r (K), of rows 2t, 2t+1, .. (V)
+    static constexpr int kPitchK = kBf16 ? 2 * D + 16 : 4 * D + 64, kPitchV = kBf16 ? 2 * D + 16 : 4 * D + 16;
+    static constexpr int kV = 16 * kPitchK, kDist = kV + 16 * kPitchV, kBytes = kDist + 16 * 4;
     static constexpr int kStages = D == 128 ? 3 : 5;             // with the scratch, what an SM has room for
-    static constexpr int kRing = kPtWarps * kStages * kBytes;
-    static constexpr int kAcc = kPtWarps * 4 * (D + 4);          // floats: four heads' states of the warps
+    static constexpr int kRing = kWarps * kStages * kBytes;
+    static constexpr int kAcc = kWarps * 4 * (D + 4);            // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
     static constexpr size_t kSmem = kRing + 4 * (size_t)kScratch;
 };
@@ -138,96 +147,272 @@ __device__ __forceinline__ void pg_cp16(uint32_t s, const void* g, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(ok ? 16 : 0) : "memory");
 }
 
-// p = hi + mid + lo, bf16 each
-__device__ __forceinline__ void split3(float p0, float p1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-    const float2 hf = __bfloat1622float2(h);
-    tc::split_bf2(p0 - hf.x, p1 - hf.y, mid, lo);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
+// x = hi + mid + lo exactly, 8 bits each, a pair of x to a register
+__device__ __forceinline__ void pg_split(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
+    hi = __byte_perm(a, b, 0x7632);
+    const float r0 = x0 - __uint_as_float(a & 0xffff0000u), r1 = x1 - __uint_as_float(b & 0xffff0000u);
+    const uint32_t c = __float_as_uint(r0), d = __float_as_uint(r1);
+    mid = __byte_perm(c, d, 0x7632);
+    lo = __byte_perm(__float_as_uint(r0 - __uint_as_float(c & 0xffff0000u)),
+                     __float_as_uint(r1 - __uint_as_float(d & 0xffff0000u)), 0x7632);
 }
 
+// The queries of a lane's rows as A fragments, and S for 16 key rows.
+template <typename T, int D, int HB>
+struct PgQ;
+
 template <int D, int HB>
-__global__ void __launch_bounds__(kPtThreads, 1)
-k_paged_tc(PgDecodeIo io) {
-    using T = __nv_bfloat16;
-    using St = PgStage<D>;
-    constexpr int S = St::kStages, P = St::kPitch;
-    constexpr int KS = D / 16, MT = D / 16;
-    constexpr int CPR = D / 8, RPI = 32 / CPR;                   // chunks per row, rows per copy instruction
+struct PgQ<__nv_bfloat16, D, HB> {
+    static constexpr int KS = D / 16, R = HB == 16 ? 2 : 1;
+    uint32_t a[KS][2 * R];
+    __device__ __forceinline__ void load(const __nv_bfloat16* q, const int (&head)[R], int gh) {
+        const int t = threadIdx.x & 3;
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const __nv_bfloat16* p = q + (size_t)head[k] * D + ks * 16 + 2 * t;
+                a[ks][k] = head[k] < gh ? __ldg(reinterpret_cast<const unsigned*>(p)) : 0u;
+                a[ks][R + k] = head[k] < gh ? __ldg(reinterpret_cast<const unsigned*>(p + 8)) : 0u;
+            }
+    }
+    __device__ __forceinline__ void ready() {}
+    __device__ __forceinline__ void logits(const unsigned char* rows, float (&x)[R][4]) const {
+        constexpr int P = PgTc<__nv_bfloat16, D>::kPitchK;
+        const int lane = threadIdx.x & 31;
+        const uint32_t kt = tc::smem_u32(rows);
+        float s[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[h][j] = 0.f;
+#pragma unroll
+        for (int kp = 0; kp < KS / 2; ++kp)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t b[4];
+                tc::ldsm4(kt + (h * 8 + (lane & 7)) * P + (kp * 32 + (lane >> 3) * 8) * 2, b);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t (&q)[2 * R] = a[2 * kp + e];
+                    tc::mma_bf16(s[h], q[0], R == 2 ? q[1] : 0u, q[R], R == 2 ? q[2 * R - 1] : 0u, b[2 * e], b[2 * e + 1]);
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[k][j] = s[j >> 1][2 * k + (j & 1)];
+    }
+};
+
+// fp32: rows 0..7 of A are the top parts, rows 8..15 the middle ones, and the
+// bottom ones an A of their own.  A chunk's 16 dims are dealt so that a lane's
+// two pairs are the four dims from 4t on.
+template <int D, int HB>
+struct PgQ<float, D, HB> {
+    static_assert(HB <= 8, "the parts of eight heads fill A");
+    static constexpr int KS = D / 16, R = 1;
+    float4 q[KS];
+    uint32_t hm[KS][4], lo[KS][2];
+    const float* src;                              // the row's query, or null: zeros
+    __device__ __forceinline__ void load(const float* first, const int (&head)[1], int gh) {
+        const int t = threadIdx.x & 3;
+        src = head[0] < gh ? first + (size_t)head[0] * D : nullptr;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            q[ks] = src != nullptr ? __ldg(reinterpret_cast<const float4*>(src + ks * 16 + 4 * t))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void ready() {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            pg_split(q[ks].x, q[ks].y, hm[ks][0], hm[ks][1], lo[ks][0]);
+            pg_split(q[ks].z, q[ks].w, hm[ks][2], hm[ks][3], lo[ks][1]);
+        }
+    }
+    __device__ __forceinline__ void logits(const unsigned char* rows, float (&x)[1][4]) const {
+        constexpr int P = PgTc<float, D>::kPitchK;
+        const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+        float s[2][2][4];                          // [slots][products of the top parts of K, the others]
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[h][0][j] = s[h][1][j] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 k = *reinterpret_cast<const float4*>(rows + (h * 8 + r) * P + (ks * 16 + 4 * t) * 4);
+                uint32_t b[3][2];
+                pg_split(k.x, k.y, b[0][0], b[1][0], b[2][0]);
+                pg_split(k.z, k.w, b[0][1], b[1][1], b[2][1]);
+                tc::mma_bf16(s[h][0], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[0][0], b[0][1]);
+                tc::mma_bf16(s[h][1], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[1][0], b[1][1]);
+                tc::mma_bf16(s[h][0], lo[ks][0], 0u, lo[ks][1], 0u, b[0][0], b[0][1]);
+                tc::mma_bf16(s[h][1], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[2][0], b[2][1]);
+            }
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float (&y)[2][4] = s[j >> 1];
+            x[0][j] = y[0][j & 1] + (y[0][2 + (j & 1)] + (y[1][j & 1] + y[1][2 + (j & 1)]));
+            odd |= x[0][j] != x[0][j];
+        }
+        // the parts of an infinity are not numbers, nor is 0 times one: as the formula has it
+        if (__any_sync(0xffffffffu, odd)) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int e = 0; e < D && src != nullptr; e += 4) {
+                const float4 z = __ldg(reinterpret_cast<const float4*>(src + e));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 k = *reinterpret_cast<const float4*>(rows + ((j >> 1) * 8 + 2 * t + (j & 1)) * P + e * 4);
+                    y[j] = fmaf(z.w, k.w, fmaf(z.z, k.z, fmaf(z.y, k.y, fmaf(z.x, k.x, y[j]))));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[0][j] = y[j];
+        }
+    }
+};
+
+// O^T += V^T P^T for 16 value rows; w[k]: the weights of row k's slots.
+template <typename T, int D, int HB>
+__device__ __forceinline__ void pg_values(const unsigned char* rows, const float (&w)[HB == 16 ? 2 : 1][4],
+                                          float (&o)[HB == 16 ? 2 : 1][D / 16][4]) {
+    constexpr int R = HB == 16 ? 2 : 1, MT = D / 16, P = PgTc<T, D>::kPitchV;
+    const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    uint32_t b[R][3][2];                           // parts of the weights, slots 2t.. and 8 + 2t..
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            pg_split(w[k][2 * h], w[k][2 * h + 1], b[k][0][h], b[k][1][h], b[k][2][h]);
+            if (HB == 4 && r >= 4) { b[k][0][h] = b[k][1][h]; b[k][2][h] = 0u; }
+        }
+    if constexpr (PgTc<T, D>::kBf16) {
+        const uint32_t va = tc::smem_u32(rows) + ((lane & 7) + ((lane >> 4) & 1) * 8) * P + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            tc::ldsm4t(va + mt * 32, a);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][0][0], b[k][0][1]);
+                if (HB != 4) tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][1][0], b[k][1][1]);
+                tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
+            }
+        }
+    } else {
+        // 32 dims at a time: a lane's four from 4r on are rows r, r + 8 of two tiles
+#pragma unroll
+        for (int c = 0; c < MT / 2; ++c) {
+            float v[4][4];                         // slots 2t, 2t+1, 8+2t, 9+2t
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(v[j]) = *reinterpret_cast<const float4*>(
+                    rows + ((j >> 1) * 8 + 2 * t + (j & 1)) * P + (c * 32 + 4 * r) * 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t a[3][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        pg_split(v[2 * h][2 * i + e], v[2 * h + 1][2 * i + e], a[0][e + 2 * h], a[1][e + 2 * h], a[2][e + 2 * h]);
+                float (&z)[4] = o[0][2 * c + i];
+                tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][0][0], b[0][0][1]);
+                tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][0][0], b[0][0][1]);
+                tc::mma_bf16(z, a[2][0], a[2][1], a[2][2], a[2][3], b[0][0][0], b[0][0][1]);
+                tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][2][0], b[0][2][1]);
+                if (HB != 4) {
+                    tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][1][0], b[0][1][1]);
+                    tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][1][0], b[0][1][1]);
+                }
+            }
+        }
+    }
+}
+
+// dim of O^T's accumulator j of tile mt in lane row r
+template <typename T, int D>
+__device__ __forceinline__ int pg_dim(int mt, int r, int j) {
+    return PgTc<T, D>::kBf16 ? mt * 16 + r + (j >> 1) * 8 : (mt >> 1) * 32 + 4 * r + (mt & 1) * 2 + (j >> 1);
+}
+
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(PgTc<T, D>::kThreads, 1)
+k_paged_decode(PgDecodeIo io) {
+    using Tc = PgTc<T, D>;
+    constexpr int S = Tc::kStages, MT = D / 16, NW = Tc::kWarps, NT = Tc::kThreads;
+    constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, RPI = 32 / CPR;     // chunks per row, rows per copy instruction
     constexpr int R = HB == 16 ? 2 : 1;                          // query rows per lane
     constexpr int LD = D + 4;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float s_ml[kPtWarps][HB][2];
+    __shared__ float s_ml[NW][HB][2];
     const PagedView& c = io.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
-    const int per = c.Hkv * c.nhb;
-    unsigned char* ring = smem + warp * S * St::kBytes;
-    float* scratch = reinterpret_cast<float*>(smem + St::kRing);
+    unsigned char* ring = smem + warp * S * Tc::kBytes;
+    float* scratch = reinterpret_cast<float*>(smem + Tc::kRing);
     const uint32_t ring_u = tc::smem_u32(ring);
-    const T* K = static_cast<const T*>(c.k) + (lane % CPR) * 8;
-    const T* V = static_cast<const T*>(c.v) + (lane % CPR) * 8;
+    const T* K = static_cast<const T*>(c.k) + (lane % CPR) * EPC;
+    const T* V = static_cast<const T*>(c.v) + (lane % CPR) * EPC;
     PgSplit sp;
     PgCursor cur;
     unsigned t0, t1;
     cudaTriggerProgrammaticLaunchCompletion();                   // the weights' kernel may come and wait
-    if (!pg_locate<kPtThreads>(c.B, per, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
+    if (!pg_locate<NT>(c.B, c.Hkv * c.nhb, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
-    int head[R], stage = 0;                                       // ring stage of the unit's first step
-    uint32_t qa[KS][2 * R];
-    float sl[R];
-    PgRaw ahead;
-    int row0, n = 0;                                              // this warp's steps: 16 list entries from row0 + i kPtStep
+    int head[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) head[k] = HB == 4 ? (r & 3) : r + 8 * k;
     PgUnit<T, D> u(io, sp, cur, t1 - t0), done = u;               // the unit at hand, the one before it
-    PgCursor at = cur;                                            // of `done`
-    float m[R], l[R], o[R][MT][4];                                // maxima, masses, accumulators of the unit
+    bool more = u.any(), handed = true;
+    PgQ<T, D, HB> q;
+    float sl[R], m[R], l[R], o[R][MT][4];                         // slopes, maxima, masses, accumulators
+    PgRaw first[S - 1], ahead;                                    // of the unit's first steps, of the next step
+    int stage = 0;                                                // ring stage of the unit's first step
 
-    auto fetch = [&](int i) {
-        return pg_fetch(io, u.ls, u.trow, u.prow, row0 + i * kPtStep + (lane & 15), i < n ? u.s1 : 0);
+    // this warp's steps of a unit: 16 list entries from row0 + i kStep, i < n
+    auto row0 = [&](const PgUnit<T, D>& x) { return x.tile * kPgTile + warp * 16; };
+    auto steps = [&](const PgUnit<T, D>& x) { return x.s1 > row0(x) ? (x.s1 - row0(x) + Tc::kStep - 1) / Tc::kStep : 0; };
+    auto fetch = [&](const PgUnit<T, D>& x, int i) {
+        const int y = row0(x) + i * Tc::kStep;
+        return pg_fetch(io, x.ls, x.trow, x.prow, y + (lane & 15), y < x.s1 ? x.s1 : 0);
     };
     auto issue = [&](int i, const PgRaw& raw) {
         float dist;
         const long long off = pg_see(io, raw, u.prow != nullptr, u.g, u.newest, dist);
-        const int at = (stage + i) % S * St::kBytes;
-        if (lane < 16) *reinterpret_cast<float*>(ring + at + 32 * P + 4 * lane) = off >= 0 ? dist : INFINITY;
+        const int at = (stage + i) % S * Tc::kBytes;
+        if (lane < 16) *reinterpret_cast<float*>(ring + at + Tc::kDist + 4 * lane) = off >= 0 ? dist : INFINITY;
 #pragma unroll
         for (int j = 0; j < 16 / RPI; ++j) {
             const int row = j * RPI + lane / CPR;
-            const long long o = __shfl_sync(0xffffffffu, off, row);
-            const uint32_t to = ring_u + at + row * P + (lane % CPR) * 16;
-            pg_cp16(to, K + (o < 0 ? 0 : o), o >= 0);
-            pg_cp16(to + 16 * P, V + (o < 0 ? 0 : o), o >= 0);
+            const long long p = __shfl_sync(0xffffffffu, off, row);
+            const uint32_t to = ring_u + at + (lane % CPR) * 16;
+            pg_cp16(to + row * Tc::kPitchK, K + (p < 0 ? 0 : p), p >= 0);
+            pg_cp16(to + Tc::kV + row * Tc::kPitchV, V + (p < 0 ? 0 : p), p >= 0);
         }
     };
-    // a unit's queries and the copies of its first steps; runs while the unit
-    // before it is handed in
-    auto begin = [&]() {
-        stage = (stage + n) % S;
-        row0 = u.tile * kPgTile + warp * 16;
-        n = u.s1 > row0 ? (u.s1 - row0 + kPtStep - 1) / kPtStep : 0;
-        PgRaw raw[S - 1];
+    if (more) {
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) raw[i] = fetch(i);
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            head[k] = HB == 4 ? (r & 3) : r + 8 * k;
-            sl[k] = u.slope2(io, head[k]);
-            const T* q = u.q + (size_t)head[k] * D + 2 * t;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qa[ks][k] = head[k] < u.gh ? __ldg(reinterpret_cast<const unsigned*>(q + ks * 16)) : 0u;
-                qa[ks][R + k] = head[k] < u.gh ? __ldg(reinterpret_cast<const unsigned*>(q + ks * 16 + 8)) : 0u;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            if (i < n) issue(i, raw[i]);
-            tc::cp_commit();
-        }
-        ahead = fetch(S - 1);
-    };
+        for (int i = 0; i < S - 1; ++i) first[i] = fetch(u, i);
+    }
 #pragma unroll 1
-    for (bool handed = true, more = u.end > u.tile;;) {
-        if (more) begin();
+    for (;;) {
+        const int n = more ? steps(u) : 0;
+        if (more) {                                               // queries and first copies: on their way during the hand-in
+            q.load(u.q, head, u.gh);
+#pragma unroll
+            for (int k = 0; k < R; ++k) sl[k] = u.slope2(io, head[k]);
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) {
+                if (i < n) issue(i, first[i]);
+                tc::cp_commit();
+            }
+            ahead = fetch(u, S - 1);
+        }
         if (!handed) {
             const PgPart<T, D> part(io, done);
 #pragma unroll
@@ -235,8 +420,8 @@ k_paged_tc(PgDecodeIo io) {
                 l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                 l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
                 if (t == 0 && (HB != 4 || r < 4)) {
-                    s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][0] = m[k];
-                    s_ml[warp][(HB == 4 ? r & 3 : r + 8 * k)][1] = l[k];
+                    s_ml[warp][head[k]][0] = m[k];
+                    s_ml[warp][head[k]][1] = l[k];
                 }
             }
             // four heads at a time through the scratch
@@ -249,17 +434,17 @@ k_paged_tc(PgDecodeIo io) {
                         float y = o[hq / 2][mt][j];
                         if (HB == 4) y += __shfl_xor_sync(0xffffffffu, y, 2);        // its parts' two columns
                         if (t / 2 == (hq & 1))
-                            scratch[(warp * 4 + (2 * t + (j & 1)) % 4) * LD + mt * 16 + r + (j >> 1) * 8] = y;
+                            scratch[(warp * 4 + (2 * t + (j & 1)) % 4) * LD + pg_dim<T, D>(mt, r, j)] = y;
                     }
                 __syncthreads();
-                for (int x = threadIdx.x; x < 4 * D; x += kPtThreads) {
+                for (int x = threadIdx.x; x < 4 * D; x += NT) {
                     const int h4 = x / D, e = x - h4 * D, h = 4 * hq + h4;
                     if (h >= done.gh) break;
                     float M = -INFINITY, A = 0.f, L = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kPtWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
+                    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][h][0]);
 #pragma unroll
-                    for (int w = 0; w < kPtWarps; ++w) {
+                    for (int w = 0; w < NW; ++w) {
                         const float mw = s_ml[w][h][0];
                         const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
                         A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
@@ -269,10 +454,23 @@ k_paged_tc(PgDecodeIo io) {
                 }
                 __syncthreads();
             }
-            pg_hand_in<T, D, kPtThreads>(io, sp, at, done, part, scratch);
+            pg_hand_in<T, D, NT>(io, sp, done, part, scratch);
         }
         if (!more) break;
         __syncthreads();                                          // the scratch has been read
+        done = u;
+        handed = false;
+        more = pg_next(io, sp, cur, done.nt, t0, t1);
+        PgUnit<T, D> next = done;
+        if (more) {
+            next = PgUnit<T, D>(io, sp, cur, t1 - t0);
+            more = next.any();
+        }
+        if (more) {                                               // its table entries, during this unit's rows
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) first[i] = fetch(next, i);
+        }
+        q.ready();
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             m[k] = -INFINITY;
@@ -287,31 +485,14 @@ k_paged_tc(PgDecodeIo io) {
             __syncwarp();                                         // stage i - 1 has been read by all lanes
             if (i + S - 1 < n) issue(i + S - 1, ahead);
             tc::cp_commit();
-            ahead = fetch(i + S);
+            ahead = fetch(u, i + S);
             tc::cp_wait<S - 1>();
             __syncwarp();
-            const int at = (stage + i) % S * St::kBytes;
-            const uint32_t kt = ring_u + at, vt = kt + 16 * P;
-            const float* dist = reinterpret_cast<const float*>(ring + at + 32 * P);
-            float s[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[h][j] = 0.f;
-#pragma unroll
-            for (int kp = 0; kp < KS / 2; ++kp)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t b[4];
-                    tc::ldsm4(kt + (h * 8 + (lane & 7)) * P + (kp * 32 + (lane >> 3) * 8) * 2, b);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t (&a)[2 * R] = qa[2 * kp + e];
-                        tc::mma_bf16(s[h], a[0], R == 2 ? a[1] : 0u, a[R], R == 2 ? a[2 * R - 1] : 0u, b[2 * e], b[2 * e + 1]);
-                    }
-                }
+            const unsigned char* rows = ring + (stage + i) % S * Tc::kBytes;
+            const float* dist = reinterpret_cast<const float*>(rows + Tc::kDist);
             // logits of this lane's rows and slots (2t, 2t+1, 8+2t, 9+2t)
             float x[R][4];
+            q.logits(rows, x);
             const float2 d0 = *reinterpret_cast<const float2*>(dist + 2 * t);
             const float2 d1 = *reinterpret_cast<const float2*>(dist + 8 + 2 * t);
             const float dd[4] = {d0.x, d0.y, d1.x, d1.y};
@@ -320,11 +501,11 @@ k_paged_tc(PgDecodeIo io) {
             for (int k = 0; k < R; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[k][j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, s[j >> 1][2 * k + (j & 1)], sl[k], dd[j]);
+                    x[k][j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j]);
                     rises |= x[k][j] > m[k] + 8.f;
                 }
             if (io.x != nullptr) {
-                const int y = row0 + i * kPtStep + 2 * t;
+                const int y = row0(u) + i * Tc::kStep + 2 * t;
 #pragma unroll
                 for (int k = 0; k < R; ++k)
                     if (head[k] < u.gh && (HB != 4 || r < 4)) {
@@ -353,214 +534,20 @@ k_paged_tc(PgDecodeIo io) {
                     }
                 }
             }
-            uint32_t b[R][3][2];                                  // parts of the weights, slots 2t.. and 8 + 2t..
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
+            for (int k = 0; k < R; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     x[k][j] = x[k][j] == -INFINITY ? 0.f : ex2(x[k][j] - m[k]);
                     l[k] += x[k][j];
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    split3(x[k][2 * h], x[k][2 * h + 1], b[k][0][h], b[k][1][h], b[k][2][h]);
-                    if (HB == 4 && r >= 4) { b[k][0][h] = b[k][1][h]; b[k][2][h] = 0u; }
-                }
-            }
-            const uint32_t va = vt + ((lane & 7) + ((lane >> 4) & 1) * 8) * P + ((lane >> 3) & 1) * 16;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                uint32_t a[4];
-                tc::ldsm4t(va + mt * 32, a);
-#pragma unroll
-                for (int k = 0; k < R; ++k) {
-                    tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][0][0], b[k][0][1]);
-                    if (HB != 4) tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][1][0], b[k][1][1]);
-                    tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
-                }
-            }
+            pg_values<T, D, HB>(rows + Tc::kV, x, o);
         }
         __syncwarp();
-        // the unit is done: its successor's first copies go out before it is handed in
-        done = u;
-        at = cur;
-        handed = false;
-        more = pg_next(io, sp, cur, u, t0, t1);
+        stage = (stage + n) % S;
+        if (more) u = next;
     }
     tc::cp_wait<0>();
-}
-
-// ---- fp32: CUDA cores --------------------------------------------------------------
-// A lane group reads UN cache rows at a time (16-byte loads; the table a step
-// ahead).  Their UN GB dot products are summed across the group's W lanes by
-// halves, so that they end spread over the lanes: a lane caps, masks and
-// exponentiates its own, and the weights come back by shuffles.
-template <int GB>
-struct PgCc {
-    static constexpr int UN = GB == 8 ? 2 : 4;
-};
-
-template <int D, int GB>
-__global__ void __launch_bounds__(kThreads, 2)
-k_paged_cc(PgDecodeIo io) {
-    using T = float;
-    using Gm = Geom<T, D>;
-    constexpr int EPC = Gm::EPC, W = Gm::CPR, GPW = Gm::GPW, NG = Gm::NG, UN = PgCc<GB>::UN;
-    // dot product x = row GB + head: the lanes x DUP / NPL .. of the group, their register x % NPL
-    constexpr int NV = UN * GB, NPL = NV > W ? NV / W : 1, DUP = NV < W ? W / NV : 1;
-    constexpr int JS = GB * DUP / NPL;         // lanes from a row to the next
-    static_assert(JS >= 1, "a lane's dot products are of one row");
-    __shared__ float sm[kWarps * GB * (D + 2)];
-    __shared__ float s_own[GB * (D + 2)];
-    __shared__ __align__(16) float s_join[kPgJoinFloats];
-    const PagedView& c = io.c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int li = lane % W, gsub = lane / W, lane0 = lane - li;
-    const int row = li / JS, head0 = li * NPL / DUP % GB;      // of this lane's dot products
-    const int per = c.Hkv * c.nhb;
-    PgSplit sp;
-    PgCursor cur;
-    unsigned t0, t1;
-    cudaTriggerProgrammaticLaunchCompletion();
-    if (!pg_locate<kThreads>(c.B, per, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
-
-    PgUnit<T, D> u(io, sp, cur, t1 - t0);
-#pragma unroll 1
-    for (bool more = u.end > u.tile; more;) {
-        const T* K = static_cast<const T*>(c.k) + li * EPC;
-        const T* V = static_cast<const T*>(c.v) + li * EPC;
-        const bool own_pos = u.prow != nullptr;
-        float qv[GB][EPC], sl[NPL];
-        PgRaw raw[UN];
-        int wt = u.tile * kPgTile + warp * UN * GPW;
-#pragma unroll
-        for (int j = 0; j < UN; ++j) raw[j] = pg_fetch(io, u.ls, u.trow, u.prow, wt + j * GPW + gsub, u.s1);
-#pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            if (h < u.gh) {
-                unpack<T>(ld_nc16(u.q + (size_t)h * D + li * EPC), qv[h]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < EPC; ++e) qv[h][e] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) sl[i] = u.slope2(io, head0 + i);
-        float m[NPL], l[NPL];
-        Online<GB, EPC> os;
-        os.init();
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
-#pragma unroll 1
-        for (; wt < u.s1; wt += UN * NG) {
-            uint4 wk[UN], wv[UN];
-            float dist = 0.f;
-            bool seen = false;                                 // of this lane's row
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                float dj;
-                const long long off = pg_see(io, raw[j], own_pos, u.g, u.newest, dj);
-                wk[j] = off >= 0 ? ld_stream16(K + off) : make_uint4(0, 0, 0, 0);
-                wv[j] = off >= 0 ? ld_stream16(V + off) : make_uint4(0, 0, 0, 0);
-                if (row == j) { dist = dj; seen = off >= 0; }
-            }
-            const int y = wt + row * GPW + gsub;
-#pragma unroll
-            for (int j = 0; j < UN; ++j)
-                raw[j] = pg_fetch(io, u.ls, u.trow, u.prow, wt + UN * NG + j * GPW + gsub, u.s1);
-            float v[NV];
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                float kf[EPC];
-                unpack<T>(wk[j], kf);
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    float x = 0.f;
-#pragma unroll
-                    for (int e = 0; e < EPC; ++e) x = fmaf(qv[h][e], kf[e], x);
-                    v[j * GB + h] = x;
-                }
-            }
-            // sums over the group's lanes: while a lane has several, it gives half away
-#pragma unroll
-            for (int off = W / 2, n = NV; off > 0; off >>= 1) {
-                if (n > 1) {
-                    n >>= 1;
-                    const bool up = (li & off) != 0;
-#pragma unroll
-                    for (int i = 0; i < n; ++i) {
-                        const float give = up ? v[i] : v[i + n];
-                        v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, give, off);
-                    }
-                } else {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-                }
-            }
-            bool rises = false;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                v[i] = seen ? pg_logit(io, v[i], sl[i], dist) : -INFINITY;
-                rises |= v[i] > m[i] + 8.f;
-                if (io.x != nullptr && li % DUP == 0 && head0 + i < u.gh && y < u.s1)
-                    io.x[(u.qh0 + head0 + i) * io.ldx + y] = v[i];
-            }
-            if (__any_sync(0xffffffffu, rises)) {
-                float sc[NPL];
-#pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    float mx = fmaxf(m[i], v[i]);
-#pragma unroll
-                    for (int off = JS; off < W; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    sc[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx);
-                    l[i] *= sc[i];
-                    m[i] = mx;
-                }
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    const float f = __shfl_sync(0xffffffffu, sc[h % NPL], lane0 + h * DUP / NPL);
-#pragma unroll
-                    for (int e = 0; e < EPC; ++e) os.acc[h][e] *= f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                v[i] = v[i] == -INFINITY ? 0.f : ex2(v[i] - m[i]);         // e^-inf: no weight
-                l[i] += v[i];
-            }
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                float vf[EPC];
-                unpack<T>(wv[j], vf);
-#pragma unroll
-                for (int h = 0; h < GB; ++h) {
-                    const int x = j * GB + h;
-                    const float p = __shfl_sync(0xffffffffu, v[x % NPL], lane0 + x * DUP / NPL);
-#pragma unroll
-                    for (int e = 0; e < EPC; ++e) os.acc[h][e] = fmaf(p, vf[e], os.acc[h][e]);
-                }
-            }
-        }
-        // the rows' sums, then every head's state in every lane of the group
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-#pragma unroll
-            for (int off = JS; off < W; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-#pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            os.m[h] = __shfl_sync(0xffffffffu, m[h % NPL], lane0 + h * DUP / NPL);
-            os.l[h] = __shfl_sync(0xffffffffu, l[h % NPL], lane0 + h * DUP / NPL);
-        }
-        warp_merge<GB, EPC, W>(os);
-        cta_merge_store<GB, EPC, W, D>(os, sm, s_own);         // m[GB], l[GB], acc[GB][D]
-        const PgPart<T, D> part(io, u);
-        for (int x = threadIdx.x; x < u.gh * D; x += kThreads) {
-            const int h = x / D, e = x - h * D;
-            part.put(io, u, h, e, s_own[2 * GB + x], s_own[h], s_own[GB + h]);
-        }
-        pg_hand_in<T, D, kThreads>(io, sp, cur, u, part, s_join);
-        __syncthreads();
-        more = pg_next(io, sp, cur, u, t0, t1);
-    }
 }
 
 // weight_out = weight + the step's attention weights summed over the group's
@@ -622,27 +609,23 @@ k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
     }
 }
 
-template <int D, int HB>
-static cudaError_t tc_launch(const PagedDecodePlan& p, const PgDecodeIo& io, cudaStream_t s) {
+template <typename T, int D, int HB>
+static cudaError_t decode_launch(const PagedDecodePlan& p, const PgDecodeIo& io, cudaStream_t s) {
+    using Tc = PgTc<T, D>;
     static std::atomic<unsigned long long> opted{0};
-    constexpr size_t smem = PgStage<D>::kSmem;
-    const cudaError_t e = opt_in_smem(k_paged_tc<D, HB>, smem, opted);
+    const cudaError_t e = opt_in_smem(k_paged_decode<T, D, HB>, Tc::kSmem, opted);
     if (e != cudaSuccess) return e;
-    k_paged_tc<D, HB><<<p.grid, kPtThreads, smem, s>>>(io);
+    k_paged_decode<T, D, HB><<<p.grid, Tc::kThreads, Tc::kSmem, s>>>(io);
     return cudaGetLastError();
 }
 
 template <int D>
-static cudaError_t decode_launch(const PagedDims& d, const PagedDecodePlan& p, const PgDecodeIo& io, cudaStream_t s) {
-    if (d.bf16) {
-        if (d.G <= 4) return tc_launch<D, 4>(p, io, s);
-        return d.G <= 8 ? tc_launch<D, 8>(p, io, s) : tc_launch<D, 16>(p, io, s);
-    }
-    if (d.G == 1) k_paged_cc<D, 1><<<p.grid, kThreads, 0, s>>>(io);
-    else if (d.G == 2) k_paged_cc<D, 2><<<p.grid, kThreads, 0, s>>>(io);
-    else if (d.G <= 4) k_paged_cc<D, 4><<<p.grid, kThreads, 0, s>>>(io);
-    else k_paged_cc<D, 8><<<p.grid, kThreads, 0, s>>>(io);
-    return cudaGetLastError();
+static cudaError_t decode_heads(const PagedDims& d, const PagedDecodePlan& p, const PgDecodeIo& io, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (d.bf16)
+        return d.G <= 4 ? decode_launch<B, D, 4>(p, io, s) : d.G <= 8 ? decode_launch<B, D, 8>(p, io, s)
+                                                                      : decode_launch<B, D, 16>(p, io, s);
+    return d.G <= 4 ? decode_launch<float, D, 4>(p, io, s) : decode_launch<float, D, 8>(p, io, s);
 }
 
 cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, const PagedDecodeArgs& a,
@@ -668,7 +651,7 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     io.local = a.local;
     io.ldx = p.ldx;
     io.extra = p.extra;
-    const cudaError_t e = d.d == 128 ? decode_launch<128>(d, p, io, s) : decode_launch<64>(d, p, io, s);
+    const cudaError_t e = d.d == 128 ? decode_heads<128>(d, p, io, s) : decode_heads<64>(d, p, io, s);
     if (e != cudaSuccess || !weights) return e;
     const long long steps = (long long)d.U() * ((d.cap + kPgWTile - 1) / kPgWTile);
     cudaLaunchConfig_t cfg = {};

@@ -2,7 +2,6 @@
 // units and their join.
 #pragma once
 
-#include "sa_cta.cuh"
 #include "sa_paged.cuh"
 
 namespace sa {
