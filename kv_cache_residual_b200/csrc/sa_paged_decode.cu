@@ -130,13 +130,15 @@ __device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp,
 template <typename T, int D>
 struct PgTc {
     static constexpr bool kBf16 = sizeof(T) == 2;
-    static constexpr int kWarps = kBf16 ? 8 : 4, kThreads = kWarps * 32;
+    // fp32 rows: as many warps as a stage ahead leaves room for (16 x 8K, 4 heads
+    // of 128: 284 us with 4 warps and 3 stages, 256 with 6 and 2)
+    static constexpr int kWarps = !kBf16 && D == 128 ? 6 : 8, kThreads = kWarps * 32;
     static constexpr int kStep = kWarps * 16;                    // list entries of a step of the CTA
     // row pitches without bank conflicts: bf16, ldmatrix; fp32, a lane's four
     // dims of row r (K), of rows 2t, 2t+1, .. (V)
     static constexpr int kPitchK = kBf16 ? 2 * D + 16 : 4 * D + 64, kPitchV = kBf16 ? 2 * D + 16 : 4 * D + 16;
     static constexpr int kV = 16 * kPitchK, kDist = kV + 16 * kPitchV, kBytes = kDist + 16 * 4;
-    static constexpr int kStages = D == 128 ? 3 : 5;             // with the scratch, what an SM has room for
+    static constexpr int kStages = !kBf16 ? 2 : D == 128 ? 3 : 5;        // with the scratch, what an SM has room for
     static constexpr int kRing = kWarps * kStages * kBytes;
     static constexpr int kAcc = kWarps * 4 * (D + 4);            // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;

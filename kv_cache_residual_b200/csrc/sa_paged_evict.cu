@@ -30,7 +30,7 @@ constexpr int kEvBins = 2048, kEvCoarse = 64;
 constexpr int kEvUn = 8;               // slots of a thread read at once
 constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory
 constexpr int kEvMoveThreads = 256;
-constexpr int kEvMoveUn = 4;           // rows in flight per lane group
+constexpr int kEvMoveUn = 4;           // rows a lane group reads at once
 
 // Order of the slots: larger keys stay.  Protected slots first, then the
 // weights as ordered integers (-0 and +0 alike), NaN as -inf.
@@ -284,55 +284,55 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     if constexpr (CL > 1) ev_sync<CL>();               // no CTA leaves while another reads its memory
 }
 
-// CTA x of a unit: its moves [x M, (x + 1) M), M = rows in flight of the CTA.
+// Warp x of a unit: its moves [32 x, 32 x + 32), whose places the lanes look up
+// one each, so that the chain count, lists, table is walked once for 32 rows.
 template <typename T, int D>
 __global__ void __launch_bounds__(kEvMoveThreads)
 k_evict_move(PagedEvictArgs a, int chunks, int moves, const int32_t* lists, const int32_t* counts) {
     using Gm = Geom<T, D>;
-    constexpr int CPR = Gm::CPR, EPC = Gm::EPC, NG = kEvMoveThreads / CPR, M = NG * kEvMoveUn;
+    constexpr int CPR = Gm::CPR, EPC = Gm::EPC, GPW = Gm::GPW, UN = kEvMoveUn;
     const PagedView& c = a.c;
-    const int u = blockIdx.x / chunks, m0 = (blockIdx.x - u * chunks) * M, b = u / c.Hkv, g = u - b * c.Hkv;
+    const int lane = threadIdx.x & 31, li = lane % CPR, gsub = lane / CPR;
+    const int x = blockIdx.x * (kEvMoveThreads / 32) + (threadIdx.x >> 5), u = x / chunks;
+    const int b = u / c.Hkv, g = u - b * c.Hkv, m = (x - u * chunks) * 32 + lane;
     cudaGridDependencySynchronize();                   // the lists
+    if (u >= c.B * c.Hkv) return;
     const int n = __ldcg(counts + u);
-    if (m0 >= n) return;
+    if (m - lane >= n) return;
     const size_t row = (size_t)u * c.ldw;
-    const int32_t* holes = lists + (size_t)u * 2 * moves;
-    const int32_t* lates = holes + moves;
+    const int32_t* lates = lists + (size_t)u * 2 * moves + moves;
     const int32_t* trow = c.table + (size_t)b * c.max_pages;
-    const int li = threadIdx.x % CPR, grp = threadIdx.x / CPR;
-    T* K = static_cast<T*>(const_cast<void*>(c.k)) + li * EPC;
-    T* V = static_cast<T*>(const_cast<void*>(c.v)) + li * EPC;
-    int src[kEvMoveUn], dst[kEvMoveUn];
-#pragma unroll
-    for (int j = 0; j < kEvMoveUn; ++j) {
-        const int m = m0 + j * NG + grp;
-        src[j] = m < n ? __ldcg(lates + m) : -1;
-        dst[j] = m < n ? __ldcg(holes + m) : -1;
-    }
-    long long from[kEvMoveUn], to[kEvMoveUn];
-#pragma unroll
-    for (int j = 0; j < kEvMoveUn; ++j) {
-        from[j] = src[j] < 0 ? -1 : pg_row(c, trow, g, src[j]);
-        to[j] = src[j] < 0 ? -1 : pg_row(c, trow, g, dst[j]);
-    }
-    uint4 wk[kEvMoveUn], wv[kEvMoveUn];
-#pragma unroll
-    for (int j = 0; j < kEvMoveUn; ++j) {
-        if (from[j] >= 0 && to[j] >= 0) {
-            wk[j] = ld_stream16(K + from[j]);
-            wv[j] = ld_stream16(V + from[j]);
-        }
-    }
-    for (int m = m0 + threadIdx.x; m < min(n, m0 + M); m += kEvMoveThreads) {
-        const int s = __ldcg(lates + m), d = __ldcg(holes + m);
+    long long from = -1, to = -1;
+    if (m < n) {
+        const int s = __ldcg(lates + m), d = __ldcg(lates + m - moves);
+        from = pg_row(c, trow, g, s);
+        to = pg_row(c, trow, g, d);
+        if (to < 0) from = -1;
         a.weight_out[row + d] = __ldg(a.weight + row + s);
         a.pos_out[row + d] = c.pos == nullptr ? s : __ldg(c.pos + row + s);
     }
+    T* K = static_cast<T*>(const_cast<void*>(c.k)) + li * EPC;
+    T* V = static_cast<T*>(const_cast<void*>(c.v)) + li * EPC;
+    const int end = min(32, n - (m - lane));
+#pragma unroll 1
+    for (int j0 = 0; j0 < end; j0 += GPW * UN) {
+        uint4 wk[UN], wv[UN];
+        long long f[UN];
 #pragma unroll
-    for (int j = 0; j < kEvMoveUn; ++j) {
-        if (from[j] >= 0 && to[j] >= 0) {
-            *reinterpret_cast<uint4*>(K + to[j]) = wk[j];
-            *reinterpret_cast<uint4*>(V + to[j]) = wv[j];
+        for (int j = 0; j < UN; ++j) {
+            f[j] = __shfl_sync(0xffffffffu, from, j0 + j * GPW + gsub);
+            if (f[j] >= 0) {
+                wk[j] = ld_stream16(K + f[j]);
+                wv[j] = ld_stream16(V + f[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+            const long long t = __shfl_sync(0xffffffffu, to, j0 + j * GPW + gsub);
+            if (f[j] >= 0) {
+                *reinterpret_cast<uint4*>(K + t) = wk[j];
+                *reinterpret_cast<uint4*>(V + t) = wv[j];
+            }
         }
     }
 }
@@ -379,9 +379,9 @@ static cudaError_t select_t(const PagedDims& d, const PagedEvictPlan& p, const P
 
 template <typename T, int D>
 static cudaError_t move_t(const PagedDims& d, const PagedEvictPlan& p, const PagedEvictArgs& a, cudaStream_t s) {
-    const int chunks = cdiv(p.moves, kEvMoveThreads / Geom<T, D>::CPR * kEvMoveUn);
+    const int chunks = cdiv(p.moves, 32);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)d.U() * chunks);
+    cfg.gridDim = dim3((unsigned)(((long long)d.U() * chunks + kEvMoveThreads / 32 - 1) / (kEvMoveThreads / 32)));
     cfg.blockDim = dim3(kEvMoveThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
