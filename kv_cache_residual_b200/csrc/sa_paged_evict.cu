@@ -25,12 +25,13 @@ namespace cg = cooperative_groups;
 namespace sa {
 
 constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048, kEvCoarse = 64;
-constexpr int kEvUn = 8;               // slots of a thread read at once
+constexpr int kEvUn = 2;               // quads of slots a thread reads at once
 constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory
 constexpr int kEvMoveThreads = 256;
 constexpr int kEvMoveUn = 4;           // rows a lane group reads at once
+
+constexpr uint32_t kEvZero = 0x80000000u;      // the key of 0; next to it, with its top digit, lie the subnormals
 
 // Order of the slots: larger keys stay.  Protected slots first, then the
 // weights as ordered integers (-0 and +0 alike), NaN as -inf.
@@ -53,15 +54,38 @@ __device__ __forceinline__ const T* ev_peer(T* p, int rank) {
     else return cg::this_cluster().map_shared_rank(p, rank);
 }
 
+// four slots from s on, s a multiple of 4 (vec: the row is aligned)
+template <typename T4, typename T>
+__device__ __forceinline__ void ev_load(T (&x)[4], const T* row, int s, int end, bool vec) {
+    if (vec && s + 4 <= end) {
+        const T4 y = __ldg(reinterpret_cast<const T4*>(row + s));
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = s + i < end ? __ldg(row + s + i) : T(0);
+    }
+}
+template <typename T4, typename T>
+__device__ __forceinline__ void ev_store(const T (&x)[4], T* row, int s, int end, bool vec) {
+    if (vec && s + 4 <= end) {
+        *reinterpret_cast<T4*>(row + s) = T4{x[0], x[1], x[2], x[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (s + i < end) row[s + i] = x[i];
+    }
+}
+
 template <int CL>
 __global__ void __launch_bounds__(kEvThreads, 2)
-k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uint32_t* far_keys) {
+k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uint32_t* far_keys, int far_row) {
+    constexpr int NT = kEvThreads, kW = NT / 32;
     extern __shared__ __align__(16) uint32_t s_mem[];
     uint32_t* s_hist = s_mem;                          // [3][kEvBins]
     __shared__ __align__(8) uint32_t s_coarse[3][kEvCoarse];
-    __shared__ uint32_t s_digit, s_above, s_equal;
-    __shared__ uint32_t s_cnt[3];                      // equal keys, freed slots, late kept slots of this slice
-    __shared__ uint32_t s_w[2][kEvWarps];
+    __shared__ uint32_t s_digit, s_above, s_equal, s_zeros, s_tiny;
+    // kept for their keys, keys equal to the last one kept, and the same of slots before `keep`
+    __shared__ uint32_t s_w[4][kW], s_cnt[4];
 
     const PagedView& c = a.c;
     const int u = blockIdx.x / CL, rank = blockIdx.x % CL, b = u / c.Hkv, g = u - b * c.Hkv;
@@ -70,6 +94,11 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     const size_t row = (size_t)u * c.ldw;
     const float* W = a.weight + row;
     const int32_t* P = c.pos == nullptr ? nullptr : c.pos + row;
+    float* Wo = a.weight_out + row;
+    int32_t* Po = a.pos_out + row;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(W) | reinterpret_cast<uintptr_t>(P) |
+                           reinterpret_cast<uintptr_t>(Wo) | reinterpret_cast<uintptr_t>(Po);
+    const bool vec = (bits & 15) == 0;
     if (threadIdx.x == 0 && rank == 0) {
         if (g == 0) a.lengths_out[b] = keep;
         if (len <= a.budget) counts[u] = 0;
@@ -79,7 +108,7 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     cudaTriggerProgrammaticLaunchCompletion();         // the moves' CTAs may come and wait
     const bool evicts = len > a.budget;
     const long long newest = pg_newest(c, b, len);
-    uint32_t* keys = far_keys == nullptr ? s_mem + 3 * kEvBins : far_keys + (size_t)u * c.cap + lo;
+    uint32_t* keys = far_keys == nullptr ? s_mem + 3 * kEvBins : far_keys + (size_t)u * far_row + lo;
     // crowded: more slots hold protected positions than may stay (positions given
     // twice), so that the weights decide among those alone
     bool crowded = false;
@@ -89,57 +118,84 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     // == prefix the first `need`
     uint32_t prefix, mask, need, equal;
     for (;;) {
-        for (int x = threadIdx.x; x < 3 * kEvBins; x += kEvThreads) s_hist[x] = 0u;
+        constexpr int kStep = 4 * kEvUn * NT;
+        float w[2][kEvUn][4];
+        int p[2][kEvUn][4];
+        auto load = [&](int k, int s0) {
+#pragma unroll
+            for (int j = 0; j < kEvUn; ++j) {
+                const int s = s0 + j * 4 * NT;
+                if (s < hi) {
+                    ev_load<float4>(w[k][j], W, s, hi, vec);
+                    if (P != nullptr) ev_load<int4>(p[k][j], P, s, hi, vec);
+                }
+            }
+        };
+        load(0, lo + 4 * threadIdx.x);
+        if (threadIdx.x == 0) s_tiny = 0u;
+        for (int x = threadIdx.x; x < 3 * kEvBins / 4; x += NT)
+            reinterpret_cast<uint4*>(s_hist)[x] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int s0 = lo + threadIdx.x; s0 < hi; s0 += kEvUn * kEvThreads) {
-            float w[kEvUn];
-            int p[kEvUn];
+#pragma unroll 1
+        for (int s0 = lo + 4 * threadIdx.x; s0 < hi; s0 += kStep) {
+            load(1, s0 + kStep);
 #pragma unroll
             for (int j = 0; j < kEvUn; ++j) {
-                const int s = s0 + j * kEvThreads;
+                const int s = s0 + j * 4 * NT;
                 if (s < hi) {
-                    w[j] = __ldg(W + s);
-                    p[j] = P == nullptr ? s : __ldg(P + s);
-                }
-            }
+                    int q[4];
 #pragma unroll
-            for (int j = 0; j < kEvUn; ++j) {
-                const int s = s0 + j * kEvThreads;
-                if (s < hi) {
+                    for (int i = 0; i < 4; ++i) q[i] = P == nullptr ? s + i : p[0][j][i];
                     // a freed slot's are written over by the move into it
-                    if (s < keep) {
-                        a.weight_out[row + s] = w[j];
-                        a.pos_out[row + s] = p[j];
-                    }
+                    ev_store<float4>(w[0][j], Wo, s, min(keep, hi), vec);
+                    ev_store<int4>(q, Po, s, min(keep, hi), vec);
                     if (evicts) {
-                        const bool always = p[j] < a.sink || newest - p[j] < a.local;
-                        const uint32_t k = crowded && !always ? 0u : ev_key(w[j], always && !crowded);
-                        keys[s - lo] = k;
-                        atomicAdd(s_hist + (k >> 21), 1u);
+                        uint32_t k[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool always = q[i] < a.sink || newest - q[i] < a.local;
+                            k[i] = crowded && !always ? 0u : ev_key(w[0][j][i], always && !crowded);
+                            // past the slice 0, which is no weight's key and never the last one kept
+                            if (s + i < hi) atomicAdd(s_hist + (k[i] >> 21), 1u); else k[i] = 0u;
+                            if (k[i] - kEvZero - 1u < (1u << 21) - 1u) s_tiny = 1u;
+                        }
+                        *reinterpret_cast<uint4*>(keys + s - lo) = make_uint4(k[0], k[1], k[2], k[3]);
                     }
                 }
             }
+#pragma unroll
+            for (int j = 0; j < kEvUn; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { w[0][j][i] = w[1][j][i]; p[0][j][i] = p[1][j][i]; }
         }
         if (!evicts) return;                           // the whole cluster
         __syncthreads();
         mask = prefix = equal = 0u;
         need = (uint32_t)keep;
+#pragma unroll 1
         for (int d = 0; d < 3 && need != equal; ++d) {
             const int sh = d == 0 ? 21 : (d == 1 ? 10 : 0);
             const uint32_t bins = d == 2 ? 1023u : 2047u;
             uint32_t* h = s_hist + d * kEvBins;
             if (d > 0) {
-                for (int s0 = threadIdx.x; s0 < hi - lo; s0 += kEvUn * kEvThreads) {
-                    uint32_t k[kEvUn];
+                for (int s0 = 4 * threadIdx.x; s0 < hi - lo; s0 += kStep) {
+                    uint4 k[kEvUn];
 #pragma unroll
-                    for (int j = 0; j < kEvUn; ++j) k[j] = s0 + j * kEvThreads < hi - lo ? keys[s0 + j * kEvThreads] : ~prefix;
+                    for (int j = 0; j < kEvUn; ++j) {
+                        const int s = s0 + j * 4 * NT;
+                        k[j] = s < hi - lo ? *reinterpret_cast<const uint4*>(keys + s) : make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
-                    for (int j = 0; j < kEvUn; ++j)
-                        if ((k[j] & mask) == prefix) atomicAdd(h + ((k[j] >> sh) & bins), 1u);
+                    for (int j = 0; j < kEvUn; ++j) {
+                        if ((k[j].x & mask) == prefix) atomicAdd(h + ((k[j].x >> sh) & bins), 1u);
+                        if ((k[j].y & mask) == prefix) atomicAdd(h + ((k[j].y >> sh) & bins), 1u);
+                        if ((k[j].z & mask) == prefix) atomicAdd(h + ((k[j].z >> sh) & bins), 1u);
+                        if ((k[j].w & mask) == prefix) atomicAdd(h + ((k[j].w >> sh) & bins), 1u);
+                    }
                 }
                 __syncthreads();
             }
-            for (int x = warp; x < kEvCoarse; x += kEvWarps) {
+            for (int x = warp; x < kEvCoarse; x += kW) {
                 const uint32_t n = __reduce_add_sync(0xffffffffu, h[x * 32 + lane]);
                 if (lane == 0) s_coarse[d][x] = n;
             }
@@ -175,7 +231,13 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
                     if (lane >= o) inc += y;
                 }
                 const int bin = __ffs(__ballot_sync(0xffffffffu, above + inc >= need)) - 1;
+                // where the last one kept has the weight 0 (a new token's) and nothing
+                // but zeros shares its digit, the key is known
+                bool tiny = false;
+                if (lane < CL) tiny = *ev_peer<CL>(&s_tiny, lane) != 0u;
+                tiny = __any_sync(0xffffffffu, tiny);
                 if (lane == bin) {
+                    s_zeros = d == 0 && !tiny && (uint32_t)(x * 32 + 31 - lane) == kEvZero >> 21 ? 1u : 0u;
                     s_digit = (uint32_t)(x * 32 + 31 - lane);
                     s_above = above + inc - n;
                     s_equal = n;
@@ -186,6 +248,10 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
             mask |= bins << sh;
             need -= s_above;
             equal = s_equal;
+            if (s_zeros != 0u) {
+                mask = 0xffffffffu;
+                break;
+            }
         }
         // more protected slots than may stay: only the protected have this key
         if (crowded || prefix != 0xffffffffu || need == equal) break;
@@ -194,100 +260,69 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     }
 
     // ---- ranks in slot order ---------------------------------------------------------
+    // Kept before slot s: those with a larger key, and of the equal ones the first
+    // `need`, so prefix counts of both kinds give every slot's place: a freed slot
+    // s < keep is number s - kept(s), a late kept one number kept(s) - kept(keep).
     // warp w takes a run of the slice, 32 slots at a time
-    const int run = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) & ~31;
+    const int run = ((hi - lo + kW - 1) / kW + 31) & ~31;
     const int w0 = min(hi, lo + warp * run), w1 = min(hi, w0 + run);
-    uint32_t eq_rank = 0u;                             // equal keys in slots before this warp's run
-    if (need < equal) {
-        uint32_t n = 0u;
+    uint32_t n[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 4
-        for (int s = w0 + lane; s < w1; s += 32) n += (keys[s - lo] & mask) == prefix ? 1u : 0u;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) s_w[0][warp] = n;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            uint32_t t = 0u;
-            for (int w = 0; w < kEvWarps; ++w) t += s_w[0][w];
-            s_cnt[0] = t;
-        }
-        ev_sync<CL>();
-#pragma unroll
-        for (int r = 0; r < CL; ++r) {
-            const uint32_t t = *ev_peer<CL>(&s_cnt[0], r);
-            eq_rank += r < rank ? t : 0u;
-        }
-        for (int w = 0; w < warp; ++w) eq_rank += s_w[0][w];
-        __syncthreads();
+    for (int s = w0 + lane; s < w1; s += 32) {
+        const uint32_t k = keys[s - lo] & mask;
+        n[0] += k > prefix ? 1u : 0u;
+        n[1] += k == prefix ? 1u : 0u;
+        n[2] += k > prefix && s < keep ? 1u : 0u;
+        n[3] += k == prefix && s < keep ? 1u : 0u;
     }
-    // calls f(slot, whether it is one, whether it stays) for the warp's slots, 32 at a time
-    auto each = [&](auto f) {
-        constexpr int UN = 4;
-        uint32_t eq = eq_rank;
-        for (int s0 = w0; s0 < w1; s0 += 32 * UN) {
-            uint32_t k[UN];
 #pragma unroll
-            for (int j = 0; j < UN; ++j) k[j] = s0 + 32 * j + lane < w1 ? keys[s0 + 32 * j + lane - lo] & mask : 0u;
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                const int s = s0 + 32 * j + lane;
-                const bool in = s < w1;
-                bool stays = in && k[j] > prefix;
-                const bool tie = in && k[j] == prefix;
-                if (need == equal) {
-                    stays |= tie;
-                } else {
-                    const unsigned ties = __ballot_sync(0xffffffffu, tie);
-                    if (tie) stays = eq + __popc(ties & ((1u << lane) - 1u)) < need;
-                    eq += __popc(ties);
-                }
-                f(s, in, stays);
-            }
-        }
-    };
-    uint32_t nh = 0u, nl = 0u;
-    each([&](int s, bool in, bool stays) {
-        nh += in && s < keep && !stays ? 1u : 0u;
-        nl += s >= keep && stays ? 1u : 0u;
-    });
-    nh = __reduce_add_sync(0xffffffffu, nh);
-    nl = __reduce_add_sync(0xffffffffu, nl);
-    if (lane == 0) { s_w[0][warp] = nh; s_w[1][warp] = nl; }
+    for (int i = 0; i < 4; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
+    if (lane < 4) s_w[lane][warp] = lane == 0 ? n[0] : lane == 1 ? n[1] : lane == 2 ? n[2] : n[3];
     __syncthreads();
-    if (threadIdx.x < 2) {
-        uint32_t t = 0u;
-        for (int w = 0; w < kEvWarps; ++w) t += s_w[threadIdx.x][w];
-        s_cnt[1 + threadIdx.x] = t;
+    if (warp < 4) {
+        const uint32_t t = __reduce_add_sync(0xffffffffu, lane < kW ? s_w[warp][lane] : 0u);
+        if (lane == 0) s_cnt[warp] = t;
     }
     ev_sync<CL>();
-    uint32_t hole = 0u, late = 0u, total = 0u;
+    uint32_t gt = 0u, eq = 0u, gt1 = 0u, eq1 = 0u;
 #pragma unroll
     for (int r = 0; r < CL; ++r) {
         const uint32_t* q = ev_peer<CL>(&s_cnt[0], r);
-        const uint32_t h = q[1], l = q[2];
-        total += h;
-        hole += r < rank ? h : 0u;
-        late += r < rank ? l : 0u;
+        gt += r < rank ? q[0] : 0u;
+        eq += r < rank ? q[1] : 0u;
+        gt1 += q[2];
+        eq1 += q[3];
     }
-    for (int w = 0; w < warp; ++w) { hole += s_w[0][w]; late += s_w[1][w]; }
-    if (threadIdx.x == 0 && rank == 0) counts[u] = (int32_t)total;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        gt += w < warp ? s_w[0][w] : 0u;
+        eq += w < warp ? s_w[1][w] : 0u;
+    }
+    const uint32_t kept1 = gt1 + min(need, eq1);       // kept(keep)
+    if (threadIdx.x == 0 && rank == 0) counts[u] = keep - (int32_t)kept1;
     int32_t* holes = lists + (size_t)u * 2 * moves;
     int32_t* lates = holes + moves;
-    each([&](int s, bool in, bool stays) {
-        const bool h = in && s < keep && !stays, l = s >= keep && stays;
-        const unsigned mh = __ballot_sync(0xffffffffu, h), ml = __ballot_sync(0xffffffffu, l);
-        const unsigned below = (1u << lane) - 1u;
-        if (h) holes[hole + __popc(mh & below)] = s;
-        if (l) lates[late + __popc(ml & below)] = s;
-        hole += __popc(mh);
-        late += __popc(ml);
-    });
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int s0 = w0; s0 < w1; s0 += 32) {
+        const int s = s0 + lane;
+        const uint32_t k = s < w1 ? keys[s - lo] & mask : 0u;
+        const bool above = s < w1 && k > prefix, tie = s < w1 && k == prefix;
+        const unsigned mg = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, tie);
+        const uint32_t ties = eq + __popc(me & below), kept = gt + __popc(mg & below) + min(need, ties);
+        const bool stays = above || (tie && ties < need);
+        if (s < keep && s < w1 && !stays) holes[s - (int)kept] = s;
+        if (s >= keep && stays) lates[kept - kept1] = s;
+        gt += __popc(mg);
+        eq += __popc(me);
+    }
     if constexpr (CL > 1) ev_sync<CL>();               // no CTA leaves while another reads its memory
 }
 
 // Warp x of a unit: its moves [32 x, 32 x + 32), whose places the lanes look up
 // one each, so that the chain count, lists, table is walked once for 32 rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kEvMoveThreads)
+__global__ void __launch_bounds__(kEvMoveThreads, 1)       // 80 registers, three CTAs per SM: more of them slow each other down
 k_evict_move(PagedEvictArgs a, int chunks, int moves, const int32_t* lists, const int32_t* counts) {
     using Gm = Geom<T, D>;
     constexpr int CPR = Gm::CPR, EPC = Gm::EPC, GPW = Gm::GPW, UN = kEvMoveUn;
@@ -350,7 +385,7 @@ PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget) {
     size_t off = 0;
     p.off_count = off; off = align256(off + sizeof(int32_t) * (size_t)d.U());
     p.off_list = off;  off = align256(off + sizeof(int32_t) * 2 * (size_t)d.U() * p.moves);
-    p.off_keys = off;  if (p.near_keys == 0) off = align256(off + sizeof(uint32_t) * (size_t)d.U() * d.cap);
+    p.off_keys = off;  if (p.near_keys == 0) off = align256(off + sizeof(uint32_t) * (size_t)d.U() * ((d.cap + 31) & ~31));
     p.bytes = off;
     return p;
 }
@@ -374,7 +409,8 @@ static cudaError_t select_t(const PagedDims& d, const PagedEvictPlan& p, const P
     cfg.numAttrs = CL > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k_evict_select<CL>, a, p.moves,
                               reinterpret_cast<int32_t*>(a.ws + p.off_list), reinterpret_cast<int32_t*>(a.ws + p.off_count),
-                              p.near_keys > 0 ? nullptr : reinterpret_cast<uint32_t*>(a.ws + p.off_keys));
+                              p.near_keys > 0 ? nullptr : reinterpret_cast<uint32_t*>(a.ws + p.off_keys),
+                              (d.cap + 31) & ~31);
 }
 
 template <typename T, int D>

@@ -666,3 +666,14 @@ def test_python_refusals():
     with pytest.raises(sa.SAError):
         sa.paged_decode(torch.zeros(2, 2, 96, dtype=BF, device=dev),
                         sa.PagedCache(d96, d96.clone(), c.table[:, :2].contiguous(), c.lengths))
+
+
+@pytest.mark.parametrize("lens", [[900, 40], [9000, 5000, 8000]])
+def test_evict_threshold_among_zeros(lens):
+    """The last one kept has the weight 0, with and without subnormals beside the zeros."""
+    for tiny in (0.0, 1e-40, -1e-40):
+        for budget in (lens[0] // 2, lens[0] - 3):
+            c = Case(lens, Hkv=1, G=1, d=64, seed=36)
+            c.weight = torch.where(c.weight < 0.8, torch.zeros_like(c.weight), c.weight)
+            c.weight[..., 7::50] = tiny
+            _evict(c, budget, 2, 5)
