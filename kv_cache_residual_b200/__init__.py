@@ -584,16 +584,11 @@ class _On:
         return False
 
 
-def _on_stream(f):
-    """f(stream handle, cache, ...) as a call f(cache, ..., stream=None) on the
-    cache's device."""
-    def call(cache, stream, *args):
-        index = cache.device.index
-        if stream is None and torch.cuda.current_device() == index:
-            return f(torch._C._cuda_getCurrentRawStream(index), cache, *args)
-        with _On(cache.device, stream) as s:
-            return f(s, cache, *args)
-    return call
+def _here(device, stream):
+    """The stream handle of a call that needs no change of device or stream, else None."""
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
 _PAGED_WS = {}
@@ -605,7 +600,7 @@ def _paged_workspace(cache, Hq, op, arg, stream):
     never share it.  A call that is being captured gets its own, whose tickets
     the graph zeroes at each replay, so that graphs replayed side by side do not
     share it either."""
-    capturing = torch.cuda.is_current_stream_capturing()
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
     if not capturing:
         ws = cache._ws.get((op, arg, Hq, stream))
         if ws is not None:
@@ -628,14 +623,6 @@ def _paged_workspace(cache, Hq, op, arg, stream):
     if not capturing:
         cache._ws[(op, arg, Hq, stream)] = ws
     return ws
-
-
-@_on_stream
-def _append(s, cache, k_new, v_new, ts, hs, start, weight):
-    status = _lib().sa_paged_append(*cache._byref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, start, k_new.shape[0],
-                                    weight, s)
-    if status != SA_OK:
-        _check(status, "sa_paged_append")
 
 
 def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
@@ -663,10 +650,17 @@ def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
         start = _dense(start, "start", torch.int32, (cache.B + 1,), device)
     if weight is not None:
         weight = _dense(weight, "weight", torch.float32, cache.slots, device)
-    _append(cache, stream, k_new, v_new, ts, hs, start, weight)
+    args = (*cache._byref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, start, N, weight)
+    s = _here(device, stream)
+    if s is not None:
+        status = _lib().sa_paged_append(*args, s)
+    else:
+        with _On(device, stream) as s:
+            status = _lib().sa_paged_append(*args, s)
+    if status != SA_OK:
+        _check(status, "sa_paged_append")
 
 
-@_on_stream
 def _decode(s, cache, q, p, Hq, weights, out, lse):
     shape = (cache.B, Hq, cache.d)
     if out is None:
@@ -710,10 +704,13 @@ def paged_decode(q, cache, scale=0.0, softcap=0.0, sink=0, local=0, slopes=None,
     if weight is not None:
         _need(weight_out is not None, "weight needs weight_out")
         p.weight = _dense(weight, "weight", torch.float32, cache.slots, dev)
-    return _decode(cache, stream, q, p, Hq, weight_out is not None, out, lse)
+    s = _here(dev, stream)
+    if s is not None:
+        return _decode(s, cache, q, p, Hq, weight_out is not None, out, lse)
+    with _On(dev, stream) as s:
+        return _decode(s, cache, q, p, Hq, weight_out is not None, out, lse)
 
 
-@_on_stream
 def _evict(s, cache, weight, budget, sink, local, lengths_out, weight_out, pos_out):
     dev, slots = cache.device, cache.slots
     if lengths_out is None:
@@ -746,7 +743,12 @@ def paged_evict(cache, weight, budget, sink=0, local=0, lengths_out=None, weight
     weight = _dense(weight, "weight", torch.float32, cache.slots, cache.device)
     _need(0 < budget < 2 ** 31, "budget must be a positive int32")
     _need(-1 < sink < 2 ** 31 and -1 < local < 2 ** 31, "sink and local must be int32, not negative")
-    return _evict(cache, stream, weight, int(budget), int(sink), int(local), lengths_out, weight_out, pos_out)
+    args = (cache, weight, int(budget), int(sink), int(local), lengths_out, weight_out, pos_out)
+    s = _here(cache.device, stream)
+    if s is not None:
+        return _evict(s, *args)
+    with _On(cache.device, stream) as s:
+        return _evict(s, *args)
 
 
 def wait_timeouts():
