@@ -553,61 +553,63 @@ k_paged_decode(PgDecodeIo io) {
 }
 
 // weight_out = weight + the step's attention weights summed over the group's
-// heads, from the logits the decode left and the rows' masses.  Four slots per
-// thread, four heads' loads of each at once; bound: HBM (or L2, where the logits
-// still are) for 4 G + 8 bytes a slot.
-constexpr int kPgWUn = 4;
-constexpr int kPgWTile = kThreads * kPgWUn;        // slots per CTA step
+// heads, from the logits the decode left and the rows' masses.  A thread takes
+// four slots in a row, as vectors where list and arrays are aligned alike.
+// Bound: HBM (or L2, where the logits still are) for 4 G + 8 bytes a slot.
+// One CTA per 1024 slots of the capacity: those past a length leave at once.
+constexpr int kPgWTile = kThreads * 4;         // slots per CTA
 
 __global__ void __launch_bounds__(kThreads)
-k_paged_weights(PgDecodeIo io, const float* weight, float* weight_out) {
+k_paged_weights(PgDecodeIo io, int tiles, const float* weight, float* weight_out) {
     const PagedView& c = io.c;
-    auto tiles = [&](int b) { return max(1, (pg_length(c, b) + kPgWTile - 1) / kPgWTile); };
-    PgSplit sp;
-    PgCursor cur;
-    unsigned t0, t1;
-    const bool any = pg_locate<kThreads>(c.B, c.Hkv, 0, blockIdx.x, tiles, sp, cur, t0, t1);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(weight_out)) & 15) == 0 &&
+                         c.ldw % 4 == 0;
+    const int unit = blockIdx.x / tiles, b = unit / c.Hkv, g = unit - b * c.Hkv;
+    const int slot = (blockIdx.x - unit * tiles) * kPgWTile + 4 * threadIdx.x;
+    const PgList ls = pg_list(c, b, io.sink, io.local);
     cudaGridDependencySynchronize();               // the logits and masses
-    if (!any) return;
-    for (unsigned t = t0; t < t1; ++t) {
-        const int b = cur.b, g = cur.sub;
-        const PgList ls = pg_list(c, b, io.sink, io.local);
-        const size_t u = (size_t)b * c.Hkv + g, row = u * c.ldw;
-        const size_t qh0 = (size_t)b * c.Hq + (size_t)g * c.G;
-        const int gap = ls.len - ls.n, first = cur.tile * kPgWTile + threadIdx.x;
-        float p[kPgWUn], w[kPgWUn];
-        int y[kPgWUn];                             // list entry, -1: not listed
+    if (slot >= ls.len) return;
+    const size_t row = (size_t)unit * c.ldw;
+    const size_t qh0 = (size_t)b * c.Hq + (size_t)g * c.G;
+    const int gap = ls.len - ls.n;
+    const bool vec = aligned && gap == 0 && slot + 4 <= ls.len;
+    float w[4], p[4] = {0.f, 0.f, 0.f, 0.f};
+    int y[4];                                  // list entries, -1: not listed
 #pragma unroll
-        for (int j = 0; j < kPgWUn; ++j) {
-            const int slot = first + j * kThreads;
-            y[j] = slot >= ls.len ? -1 : slot < ls.s_eff ? slot : slot >= ls.s_eff + gap ? slot - gap : -1;
-            w[j] = slot < ls.len && weight != nullptr ? weight[row + slot] : 0.f;
-            p[j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+        const int s = slot + j;
+        y[j] = s >= ls.len ? -1 : s < ls.s_eff ? s : s >= ls.s_eff + gap ? s - gap : -1;
+        w[j] = 0.f;
+    }
+    if (weight != nullptr) {
+        if (vec) {
+            *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(weight + row + slot);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (slot + j < ls.len) w[j] = weight[row + slot + j];
         }
-        for (int h = 0; h < c.G; h += 4) {
-            float x[4][kPgWUn], l2[4];
+    }
+#pragma unroll 4
+    for (int h = 0; h < c.G; ++h) {
+        const float l2 = __ldcg(io.lse2 + qh0 + h);
+        const float* xs = io.x + (qh0 + h) * io.ldx;
+        float x[4];
+        if (vec) {
+            *reinterpret_cast<float4*>(x) = __ldcg(reinterpret_cast<const float4*>(xs + slot));
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                l2[k] = h + k < c.G ? __ldcg(io.lse2 + qh0 + h + k) : 0.f;
-                const float* xs = io.x + (qh0 + h + k) * io.ldx;
-#pragma unroll
-                for (int j = 0; j < kPgWUn; ++j) x[k][j] = h + k < c.G && y[j] >= 0 ? __ldcg(xs + y[j]) : -INFINITY;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < kPgWUn; ++j) p[j] += x[k][j] == -INFINITY ? 0.f : ex2(x[k][j] - l2[k]);
+            for (int j = 0; j < 4; ++j) x[j] = y[j] >= 0 ? __ldcg(xs + y[j]) : -INFINITY;
         }
 #pragma unroll
-        for (int j = 0; j < kPgWUn; ++j) {
-            const int slot = first + j * kThreads;
-            if (slot < ls.len) weight_out[row + slot] = w[j] + p[j];
-        }
-        const int nt = tiles(b);
-        if (++cur.tile == nt) {
-            cur.tile = 0;
-            if (++cur.sub == c.Hkv) { cur.sub = 0; ++cur.b; }
-        }
+        for (int j = 0; j < 4; ++j) p[j] += x[j] == -INFINITY ? 0.f : ex2(x[j] - l2);
+    }
+    if (vec) {
+        *reinterpret_cast<float4*>(weight_out + row + slot) = make_float4(w[0] + p[0], w[1] + p[1], w[2] + p[2], w[3] + p[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (slot + j < ls.len) weight_out[row + slot + j] = w[j] + p[j];
     }
 }
 
@@ -655,9 +657,9 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     io.extra = p.extra;
     const cudaError_t e = d.d == 128 ? decode_heads<128>(d, p, io, s) : decode_heads<64>(d, p, io, s);
     if (e != cudaSuccess || !weights) return e;
-    const long long steps = (long long)d.U() * ((d.cap + kPgWTile - 1) / kPgWTile);
+    const int tiles = cdiv(d.cap, kPgWTile);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(steps < 148 * 8 ? steps : 148 * 8));
+    cfg.gridDim = dim3((unsigned)d.U() * tiles);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -665,7 +667,7 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_weights, io, a.weight, a.weight_out);
+    return cudaLaunchKernelEx(&cfg, k_paged_weights, io, tiles, a.weight, a.weight_out);
 }
 
 }  // namespace sa
