@@ -677,3 +677,16 @@ def test_evict_threshold_among_zeros(lens):
             c.weight = torch.where(c.weight < 0.8, torch.zeros_like(c.weight), c.weight)
             c.weight[..., 7::50] = tiny
             _evict(c, budget, 2, 5)
+
+
+@pytest.mark.parametrize("lens,Hkv,dtype", [
+    ([int(x) for x in np.random.default_rng(70).integers(2000, 4000, 40)], 8, BF),      # several units a CTA
+    ([910001], 1, BF),                                                                  # one unit over all CTAs
+    ([int(x) for x in np.random.default_rng(71).integers(0, 41, 1000)], 4, F32),        # many units of one tile
+], ids=["several", "one", "short"])
+def test_decode_much_work(lens, Hkv, dtype):
+    c = Case(lens, Hkv=Hkv, G=2, d=64, dtype=dtype, cols=-(-max(lens) // 16), seed=72)
+    out, lse = _decode(c, weights=len(lens) < 100)
+    for _ in range(3):
+        again = sa.paged_decode(c.q, c.cache())
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
