@@ -279,7 +279,10 @@ struct PgQ<float, D, HB> {
     }
 };
 
-// O^T += V^T P^T for 16 value rows; w[k]: the weights of row k's slots.
+// O^T += V^T P^T for 16 value rows; w[k]: the weights of row k's slots.  A matrix
+// instruction cuts its sum off where fp32 ends instead of rounding it, which over
+// thousands of rows adds up on one side (8e-6 of the output after 32K), so each
+// step's sum begins at zero and is added by an ordinary addition.
 template <typename T, int D, int HB>
 __device__ __forceinline__ void pg_values(const unsigned char* rows, const float (&w)[HB == 16 ? 2 : 1][4],
                                           float (&o)[HB == 16 ? 2 : 1][D / 16][4]) {
@@ -301,9 +304,12 @@ __device__ __forceinline__ void pg_values(const unsigned char* rows, const float
             tc::ldsm4t(va + mt * 32, a);
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][0][0], b[k][0][1]);
-                if (HB != 4) tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][1][0], b[k][1][1]);
-                tc::mma_bf16(o[k][mt], a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
+                if (HB != 4) tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][1][0], b[k][1][1]);
+                tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][0][0], b[k][0][1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[k][mt][j] += z[j];
             }
         }
     } else {
@@ -323,15 +329,17 @@ __device__ __forceinline__ void pg_values(const unsigned char* rows, const float
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         pg_split(v[2 * h][2 * i + e], v[2 * h + 1][2 * i + e], a[0][e + 2 * h], a[1][e + 2 * h], a[2][e + 2 * h]);
-                float (&z)[4] = o[0][2 * c + i];
-                tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][0][0], b[0][0][1]);
-                tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][0][0], b[0][0][1]);
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
                 tc::mma_bf16(z, a[2][0], a[2][1], a[2][2], a[2][3], b[0][0][0], b[0][0][1]);
                 tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][2][0], b[0][2][1]);
                 if (HB != 4) {
-                    tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][1][0], b[0][1][1]);
                     tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][1][0], b[0][1][1]);
+                    tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][1][0], b[0][1][1]);
                 }
+                tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][0][0], b[0][0][1]);
+                tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][0][0], b[0][0][1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[0][2 * c + i][j] += z[j];
             }
         }
     }
