@@ -457,13 +457,15 @@ SA_API sa_status sa_dense_decode(const sa_shape* shape, const void* q, const voi
  * table[b, s / page].  A slot's position is the index of its token in the
  * sequence; eviction moves tokens between slots, and `pos` then says which
  * token a slot holds.  Lengths, tables and positions are read on the device
- * by each call, so a call captured in a CUDA graph follows them at replay.
+ * by each call, so a call captured in a CUDA graph follows them at replay; they
+ * must not be written while a call runs.
  * The method has no counterpart: these are the dense operators a serving
  * program needs beside the sparse ones.
  *
  * Supported: d in {64, 128}; any Hq / Hkv; any page size; B * Hkv < 65536,
  * B * Hq < 2^24, max_pages * page <= 2^30 (the capacity in slots of a
- * sequence, `cap` below); fewer than 2^31 64-slot tiles in all.  Strides are
+ * sequence, `cap` below); fewer than 2^31 64-slot tiles in all (and eight for
+ * every KV head of every sequence).  Strides are
  * in elements of dtype, positive multiples of 16 bytes; a row's d elements
  * are contiguous; 0 for all three = the dense pool
  * [n_pages, Hkv, page, d] (row_stride d, head_stride page d, page_stride
@@ -549,7 +551,10 @@ SA_API sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cac
  *   lse[b, h] = ln sum_s exp(x_hs),  out[b, h, :] = sum_s exp(x_hs - lse) v_s
  * over the visible slots (out [B, Hq, d] f32, lse [B, Hq] f32 or NULL).  A
  * row that sees nothing (length 0, a window that leaves none, no valid page)
- * gives out = 0, lse = -inf and adds no weight.  q [B, Hq, d] in dtype. */
+ * gives out = 0, lse = -inf and adds no weight.  q [B, Hq, d] in dtype.  Keys
+ * and values of slots that are not seen are not read; of those seen, a key's
+ * infinities count as the formula has them (a logit of -inf is no weight), a
+ * value that is not finite gives NaN. */
 SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cache,
                                  const sa_paged_params* params, const void* q, float* out, float* lse, void* ws,
                                  size_t ws_bytes, void* stream);

@@ -15,6 +15,7 @@ Layouts: k, v [B, Hkv, L, d]; q_ctx [B, Hq, L, d]; q [B, Hq, d]; bf16 or fp32
 """
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -516,7 +517,8 @@ class PagedCache:
     and seen [B] int32 together, or neither (no token has been evicted).
 
     The object holds the tensors and reads nothing from them: their values may
-    change between calls, and between replays of a captured one."""
+    change between calls, and between replays of a captured one.  Other tensors
+    make another cache."""
 
     def __init__(self, k, v, table, lengths, pos=None, seen=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device and k.is_cuda,
@@ -528,7 +530,7 @@ class PagedCache:
         self.dtype, self.device = k.dtype, k.device
         self.slots = torch.Size((self.B, self.Hkv, self.capacity))      # of pos and of the weights
         self._ws = {}
-        self.k, self.v, self.table, self.lengths, self.pos, self.seen = k, v, table, lengths, pos, seen
+        self._tensors = k, v, table, lengths, pos, seen
         strides = []
         for t in (k, v):
             _need(t.stride(3) == 1, "the rows of k and v must be contiguous")
@@ -549,6 +551,14 @@ class PagedCache:
         self._shape = sa_paged_shape(self.B, self.Hkv, self.Hkv, self.d, _dtype_code(k), self.n_pages, self.page,
                                      self.max_pages, 0, *strides[0])
         self._byref = (ctypes.byref(self._shape), ctypes.byref(c))
+
+    # the calls hold the tensors' addresses, so these are not to be set
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    table = property(lambda self: self._tensors[2])
+    lengths = property(lambda self: self._tensors[3])
+    pos = property(lambda self: self._tensors[4])
+    seen = property(lambda self: self._tensors[5])
 
     def _for_heads(self, Hq):
         """The C shape with Hq query heads."""
@@ -592,6 +602,7 @@ def _here(device, stream):
 
 
 _PAGED_WS = {}
+_PAGED_LOCK = threading.Lock()      # a call's kernels follow one another on its stream, whoever else calls
 
 
 def _paged_workspace(cache, Hq, op, arg, stream):
@@ -669,8 +680,9 @@ def _decode(s, cache, q, p, Hq, weights, out, lse):
         lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
     po = _dense(out, "out", torch.float32, shape, cache.device)
     pl = _dense(lse, "lse", torch.float32, shape[:2], cache.device)
-    ws = _paged_workspace(cache, Hq, OP_PAGED_DECODE, weights, s)
-    status = _lib().sa_paged_decode(ws[1], cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl, ws[2], ws[3], s)
+    with _PAGED_LOCK:
+        ws = _paged_workspace(cache, Hq, OP_PAGED_DECODE, weights, s)
+        status = _lib().sa_paged_decode(ws[1], cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl, ws[2], ws[3], s)
     if status != SA_OK:
         _check(status, "sa_paged_decode")
     return out, lse
@@ -722,8 +734,9 @@ def _evict(s, cache, weight, budget, sink, local, lengths_out, weight_out, pos_o
     po = (_dense(lengths_out, "lengths_out", torch.int32, (cache.B,), dev),
           _dense(weight_out, "weight_out", torch.float32, slots, dev),
           _dense(pos_out, "pos_out", torch.int32, slots, dev))
-    ws = _paged_workspace(cache, cache.Hkv, OP_PAGED_EVICT, budget, s)
-    status = _lib().sa_paged_evict(*cache._byref, weight, budget, sink, local, *po, ws[2], ws[3], s)
+    with _PAGED_LOCK:
+        ws = _paged_workspace(cache, cache.Hkv, OP_PAGED_EVICT, budget, s)
+        status = _lib().sa_paged_evict(*cache._byref, weight, budget, sink, local, *po, ws[2], ws[3], s)
     if status != SA_OK:
         _check(status, "sa_paged_evict")
     return lengths_out, weight_out, pos_out

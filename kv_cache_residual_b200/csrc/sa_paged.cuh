@@ -119,7 +119,7 @@ __device__ __forceinline__ bool pg_locate(int B, int per, int extra, unsigned i,
     if (t0 >= before * per && t0 < (before + sum) * per) {      // this thread's sequences hold t0
         unsigned base = before;
         int b = b0;
-        for (;; ++b) {
+        for (; b < b1 - 1; ++b) {
             const unsigned n = tiles(b) + E;
             if (t0 < (base + n) * per) break;
             base += n;
@@ -130,7 +130,7 @@ __device__ __forceinline__ bool pg_locate(int B, int per, int extra, unsigned i,
     __syncthreads();
     cur.b = s_b;
     const unsigned n = tiles(cur.b) + E, x = t0 - s_base * per;
-    cur.sub = (int)(x / n);
+    cur.sub = min((int)(x / n), per - 1);
     cur.tile = (int)(x - cur.sub * n);
     cur.unit0 = t0 - cur.tile;
     return true;

@@ -106,12 +106,16 @@ sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cac
         (p.weight != nullptr && (!aligned4(p.weight) || p.weight_out == nullptr)) ||
         (p.weight_out != nullptr && !aligned4(p.weight_out)))
         return SA_ERR_INVALID_ARG;
+    // what the kernel multiplies by has to be a number
+    const float scale = resolve_scale(p.scale, d.d);
+    if (!(scale * 1.5f < INFINITY) || (p.softcap > 0.f && !(scale / p.softcap < INFINITY && p.softcap * 1.5f < INFINITY)))
+        return SA_ERR_INVALID_ARG;
     const long long qs = p.q_stride == 0 ? (long long)d.Hq * d.d : p.q_stride;
     if (!strides_ok(qs, d)) return SA_ERR_INVALID_ARG;
     const PagedDecodePlan plan = paged_decode_plan(d, p.weight_out != nullptr);
     if (ws == nullptr || ws_bytes < plan.bytes || !aligned16(ws)) return SA_ERR_WORKSPACE;
     const PagedDecodeArgs a{paged_view(d, *cache), q, qs, p.slopes, p.weight, p.weight_out, out, lse,
-                            resolve_scale(p.scale, d.d), p.softcap, p.sink, p.local, static_cast<char*>(ws)};
+                            scale, p.softcap, p.sink, p.local, static_cast<char*>(ws)};
     return launch_paged_decode(d, plan, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -126,7 +130,7 @@ sa_status sa_paged_evict(const sa_paged_shape* shape, const sa_paged_cache* cach
         !aligned4(pos_out))
         return SA_ERR_INVALID_ARG;
     if (budget < 1 || sink < 0 || local < 0 || (long long)sink + local > budget) return SA_ERR_INVALID_ARG;
-    if (lengths_out == cache->lengths || weight_out == weight || pos_out == cache->pos) return SA_ERR_INVALID_ARG;
+    if (lengths_out == cache->lengths || lengths_out == cache->seen || weight_out == weight || pos_out == cache->pos) return SA_ERR_INVALID_ARG;
     const PagedEvictPlan plan = paged_evict_plan(d, budget);
     if (ws == nullptr || ws_bytes < plan.bytes || !aligned16(ws)) return SA_ERR_WORKSPACE;
     const PagedEvictArgs a{paged_view(d, *cache), weight, budget, sink, local, lengths_out, weight_out, pos_out,

@@ -105,7 +105,7 @@ __device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp,
     cur.unit0 += n;
     cur.tile = 0;
     if (++cur.sub == io.c.Hkv * io.c.nhb) { cur.sub = 0; ++cur.b; }
-    return true;
+    return cur.b < io.c.B;
 }
 
 // ---- the pass --------------------------------------------------------------------

@@ -690,3 +690,38 @@ def test_decode_much_work(lens, Hkv, dtype):
     for _ in range(3):
         again = sa.paged_decode(c.q, c.cache())
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_a_cache_keeps_its_tensors():
+    c = Case([20], seed=80)
+    cache = c.cache()
+    with pytest.raises(AttributeError):
+        cache.lengths = c.lengths.clone()
+    assert cache.lengths is c.lengths and cache.k is c.k
+
+
+def test_threads_on_one_stream():
+    """Calls of two threads on one stream share its scratch one after another."""
+    import threading
+    cs = [Case([3000, 40], seed=81), Case([3000, 40], seed=82)]
+    want = []
+    for c in cs:
+        wo = torch.zeros_like(c.weight)
+        want.append((*sa.paged_decode(c.q, c.cache(), weight=c.weight, weight_out=wo), wo))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        for _ in range(40):
+            wo = torch.zeros_like(c.weight)
+            got = (*sa.paged_decode(c.q, c.cache(), weight=c.weight, weight_out=wo), wo)
+            torch.cuda.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                bad.append(c)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(cs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad

@@ -167,3 +167,13 @@ def test_python_refuses_host_tensors():
     k = torch.zeros(4, 2, 16, 64)
     with pytest.raises(ValueError):
         sa.PagedCache(k, k.clone(), torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_factors_that_overflow_are_refused():
+    bad = sa.SA_ERR_INVALID_ARG
+    for kw in (dict(scale=3.3e38), dict(softcap=1e-45), dict(softcap=3.3e38), dict(scale=1e30, softcap=1e-20)):
+        assert _decode(params=_params(**kw)) == bad, kw
+
+
+def test_evict_refuses_to_write_over_seen():
+    assert _evict(cache=_cache(pos=0x30000, seen=0x20000)) == sa.SA_ERR_INVALID_ARG
