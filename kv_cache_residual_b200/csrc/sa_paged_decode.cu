@@ -149,6 +149,19 @@ __device__ __forceinline__ void pg_cp16(uint32_t s, const void* g, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(ok ? 16 : 0) : "memory");
 }
 
+// d = a b on the matrix unit, from zero.  A matrix instruction cuts its sum off
+// where fp32 ends instead of rounding it, which over many adds up on one side
+// (8e-6 of the output after 32K rows), so sums begin anew every few instructions
+// and are added up by ordinary additions.
+__device__ __forceinline__ void pg_mma0(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // x = hi + mid + lo exactly, 8 bits each, a pair of x to a register
 __device__ __forceinline__ void pg_split(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
@@ -180,7 +193,7 @@ struct PgQ<__nv_bfloat16, D, HB> {
             }
     }
     __device__ __forceinline__ void ready() {}
-    __device__ __forceinline__ void logits(const unsigned char* rows, float (&x)[R][4]) const {
+    __device__ __forceinline__ void dots(const unsigned char* rows, float (&x)[R][4]) const {
         constexpr int P = PgTc<__nv_bfloat16, D>::kPitchK;
         const int lane = threadIdx.x & 31;
         const uint32_t kt = tc::smem_u32(rows);
@@ -195,11 +208,12 @@ struct PgQ<__nv_bfloat16, D, HB> {
             for (int h = 0; h < 2; ++h) {
                 uint32_t b[4];
                 tc::ldsm4(kt + (h * 8 + (lane & 7)) * P + (kp * 32 + (lane >> 3) * 8) * 2, b);
+                float z[4];
+                const uint32_t (&q0)[2 * R] = a[2 * kp], (&q1)[2 * R] = a[2 * kp + 1];
+                pg_mma0(z, q0[0], R == 2 ? q0[1] : 0u, q0[R], R == 2 ? q0[2 * R - 1] : 0u, b[0], b[1]);
+                tc::mma_bf16(z, q1[0], R == 2 ? q1[1] : 0u, q1[R], R == 2 ? q1[2 * R - 1] : 0u, b[2], b[3]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t (&q)[2 * R] = a[2 * kp + e];
-                    tc::mma_bf16(s[h], q[0], R == 2 ? q[1] : 0u, q[R], R == 2 ? q[2 * R - 1] : 0u, b[2 * e], b[2 * e + 1]);
-                }
+                for (int j = 0; j < 2 * R; ++j) s[h][j] += z[j];
             }
 #pragma unroll
         for (int k = 0; k < R; ++k)
@@ -233,10 +247,10 @@ struct PgQ<float, D, HB> {
             pg_split(q[ks].z, q[ks].w, hm[ks][2], hm[ks][3], lo[ks][1]);
         }
     }
-    __device__ __forceinline__ void logits(const unsigned char* rows, float (&x)[1][4]) const {
+    __device__ __forceinline__ void dots(const unsigned char* rows, float (&x)[1][4]) const {
         constexpr int P = PgTc<float, D>::kPitchK;
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-        float s[2][2][4];                          // [slots][products of the top parts of K, the others]
+        float s[2][2][4];                          // [slots][products of top parts with them, the others]
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -249,10 +263,13 @@ struct PgQ<float, D, HB> {
                 uint32_t b[3][2];
                 pg_split(k.x, k.y, b[0][0], b[1][0], b[2][0]);
                 pg_split(k.z, k.w, b[0][1], b[1][1], b[2][1]);
-                tc::mma_bf16(s[h][0], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[0][0], b[0][1]);
-                tc::mma_bf16(s[h][1], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[1][0], b[1][1]);
-                tc::mma_bf16(s[h][0], lo[ks][0], 0u, lo[ks][1], 0u, b[0][0], b[0][1]);
+                float z[4];
+                pg_mma0(z, hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[0][0], b[0][1]);
                 tc::mma_bf16(s[h][1], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[2][0], b[2][1]);
+                tc::mma_bf16(s[h][1], lo[ks][0], 0u, lo[ks][1], 0u, b[0][0], b[0][1]);
+                tc::mma_bf16(s[h][1], hm[ks][0], hm[ks][1], hm[ks][2], hm[ks][3], b[1][0], b[1][1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[h][0][j] += z[j];
             }
         bool odd = false;
 #pragma unroll
@@ -279,10 +296,7 @@ struct PgQ<float, D, HB> {
     }
 };
 
-// O^T += V^T P^T for 16 value rows; w[k]: the weights of row k's slots.  A matrix
-// instruction cuts its sum off where fp32 ends instead of rounding it, which over
-// thousands of rows adds up on one side (8e-6 of the output after 32K), so each
-// step's sum begins at zero and is added by an ordinary addition.
+// O^T += V^T P^T for 16 value rows; w[k]: the weights of row k's slots.
 template <typename T, int D, int HB>
 __device__ __forceinline__ void pg_values(const unsigned char* rows, const float (&w)[HB == 16 ? 2 : 1][4],
                                           float (&o)[HB == 16 ? 2 : 1][D / 16][4]) {
@@ -304,8 +318,8 @@ __device__ __forceinline__ void pg_values(const unsigned char* rows, const float
             tc::ldsm4t(va + mt * 32, a);
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
+                float z[4];
+                pg_mma0(z, a[0], a[1], a[2], a[3], b[k][2][0], b[k][2][1]);
                 if (HB != 4) tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][1][0], b[k][1][1]);
                 tc::mma_bf16(z, a[0], a[1], a[2], a[3], b[k][0][0], b[k][0][1]);
 #pragma unroll
@@ -329,8 +343,8 @@ __device__ __forceinline__ void pg_values(const unsigned char* rows, const float
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         pg_split(v[2 * h][2 * i + e], v[2 * h + 1][2 * i + e], a[0][e + 2 * h], a[1][e + 2 * h], a[2][e + 2 * h]);
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                tc::mma_bf16(z, a[2][0], a[2][1], a[2][2], a[2][3], b[0][0][0], b[0][0][1]);
+                float z[4];
+                pg_mma0(z, a[2][0], a[2][1], a[2][2], a[2][3], b[0][0][0], b[0][0][1]);
                 tc::mma_bf16(z, a[0][0], a[0][1], a[0][2], a[0][3], b[0][2][0], b[0][2][1]);
                 if (HB != 4) {
                     tc::mma_bf16(z, a[1][0], a[1][1], a[1][2], a[1][3], b[0][1][0], b[0][1][1]);
@@ -500,40 +514,53 @@ k_paged_decode(PgDecodeIo io) {
             __syncwarp();
             const unsigned char* rows = ring + (stage + i) % S * Tc::kBytes;
             const float* dist = reinterpret_cast<const float*>(rows + Tc::kDist);
-            // logits of this lane's rows and slots (2t, 2t+1, 8+2t, 9+2t)
+            // dot products of this lane's rows and slots (2t, 2t+1, 8+2t, 9+2t)
             float x[R][4];
-            q.logits(rows, x);
+            q.dots(rows, x);
             const float2 d0 = *reinterpret_cast<const float2*>(dist + 2 * t);
             const float2 d1 = *reinterpret_cast<const float2*>(dist + 8 + 2 * t);
             const float dd[4] = {d0.x, d0.y, d1.x, d1.y};
+            // relative to the maximum so far, which is moved when one passes it by 8
+            float p[R][4];
             bool rises = false;
 #pragma unroll
-            for (int k = 0; k < R; ++k)
+            for (int k = 0; k < R; ++k) {
+                const float ref = m[k] == -INFINITY ? 0.f : m[k], over = m[k] == -INFINITY ? -INFINITY : 8.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[k][j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j]);
-                    rises |= x[k][j] > m[k] + 8.f;
+                    x[k][j] = pg_cap(io, x[k][j]);
+                    p[k][j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j], ref);
+                    rises |= p[k][j] > over;
                 }
+            }
             if (io.x != nullptr) {
                 const int y = row0(u) + i * Tc::kStep + 2 * t;
 #pragma unroll
                 for (int k = 0; k < R; ++k)
                     if (head[k] < u.gh && (HB != 4 || r < 4)) {
                         float* xs = io.x + (u.qh0 + head[k]) * io.ldx + y;      // rows of whole tiles: both pairs fit
-                        *reinterpret_cast<float2*>(xs) = make_float2(x[k][0], x[k][1]);
-                        *reinterpret_cast<float2*>(xs + 8) = make_float2(x[k][2], x[k][3]);
+                        float z[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            z[j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j], 0.f);
+                        *reinterpret_cast<float2*>(xs) = make_float2(z[0], z[1]);
+                        *reinterpret_cast<float2*>(xs + 8) = make_float2(z[2], z[3]);
                     }
             }
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    float mx = fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3]));
+                    const float ref = m[k] == -INFINITY ? 0.f : m[k];
+                    float mx = fmaxf(fmaxf(p[k][0], p[k][1]), fmaxf(p[k][2], p[k][3]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    mx = fmaxf(mx, m[k]);
+                    mx = fmaxf(m[k], ref + mx);
                     const float sc = m[k] == -INFINITY ? 0.f : ex2(m[k] - mx);
                     m[k] = mx;
                     l[k] *= sc;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        p[k][j] = dd[j] == INFINITY || mx == -INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j], mx);
                     const float c0 = __shfl_sync(0xffffffffu, sc, 8 * t), c1 = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -548,10 +575,10 @@ k_paged_decode(PgDecodeIo io) {
             for (int k = 0; k < R; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[k][j] = x[k][j] == -INFINITY ? 0.f : ex2(x[k][j] - m[k]);
-                    l[k] += x[k][j];
+                    p[k][j] = p[k][j] == -INFINITY ? 0.f : ex2(p[k][j]);
+                    l[k] += p[k][j];
                 }
-            pg_values<T, D, HB>(rows + Tc::kV, x, o);
+            pg_values<T, D, HB>(rows + Tc::kV, p, o);
         }
         __syncwarp();
         stage = (stage + n) % S;
@@ -654,11 +681,9 @@ cudaError_t launch_paged_decode(const PagedDims& d, const PagedDecodePlan& p, co
     io.x = weights ? reinterpret_cast<float*>(a.ws + p.off_x) : nullptr;
     io.rec = reinterpret_cast<float*>(a.ws + p.off_rec);
     io.cnt = reinterpret_cast<unsigned*>(a.ws + p.off_cnt);
-    io.scale = a.scale;
-    io.qscale = a.scale * kLog2e;
     io.softcap = a.softcap;
     io.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-    io.cap_out = a.softcap * kLog2e;
+    io.factor = (a.softcap > 0.f ? a.softcap : a.scale) * kLog2e;
     io.sink = a.sink;
     io.local = a.local;
     io.ldx = p.ldx;

@@ -17,16 +17,20 @@ struct PgDecodeIo {
     float* x;                // with weights: logits (log2) [B, Hq, ldx] of the listed slots, or null
     float* rec;              // two records per CTA
     unsigned* cnt;           // completion tickets, one per unit
-    float scale, qscale;     // softmax scale, and times log2(e)
-    float softcap, cap_in, cap_out;    // c, scale / c, c log2(e)
+    float softcap, cap_in;   // c, scale / c
+    float factor;            // log2(e) times the scale, or times c
     int sink, local, ldx, extra;
 };
 
-// logit in log2 units: the dot product scaled, capped (tanhf: 2 ulp, so that
-// the capped logit is as exact as the dot product), and biased by distance
-__device__ __forceinline__ float pg_logit(const PgDecodeIo& io, float dot, float slope2, float dist) {
-    const float x = io.softcap > 0.f ? io.cap_out * tanhf(dot * io.cap_in) : dot * io.qscale;
-    return fmaf(-slope2, dist, x);
+// A logit in log2 units less `ref`: factor c - slope2 dist - ref, with c the dot
+// product, or its tanh where logits are capped (tanhf: 2 ulp, so that a capped
+// logit is as exact as the dot product).  Taking ref (the running maximum) off
+// inside the fused operations leaves no rounding of the size of the logit.
+__device__ __forceinline__ float pg_cap(const PgDecodeIo& io, float dot) {
+    return io.softcap > 0.f ? tanhf(dot * io.cap_in) : dot;
+}
+__device__ __forceinline__ float pg_logit(const PgDecodeIo& io, float c, float slope2, float dist, float ref) {
+    return fmaf(-slope2, dist, fmaf(c, io.factor, -ref));
 }
 
 // What a lane reads of a listed slot: its page, and its position where slots
@@ -65,9 +69,9 @@ __device__ __forceinline__ float* pg_rec(float* rec, int floats, int cta, bool b
 
 // a head's log of its mass L 2^M
 __device__ __forceinline__ void pg_write_lse(const PgDecodeIo& io, size_t qh, float M, float L) {
-    const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
-    if (io.lse != nullptr) io.lse[qh] = l2 * kLn2;
-    if (io.x != nullptr) io.lse2[qh] = l2;
+    constexpr float kLn2Rest = -1.9046543e-9f;     // ln 2 - kLn2
+    if (io.lse != nullptr) io.lse[qh] = L == 0.f ? -INFINITY : fmaf(M, kLn2, fmaf(M, kLn2Rest, logf(L)));
+    if (io.x != nullptr) io.lse2[qh] = L == 0.f ? -INFINITY : M + log2f(L);
 }
 
 // 1 / L, and 0 where nothing is seen (out = A inv: one rounding more than A / L)
