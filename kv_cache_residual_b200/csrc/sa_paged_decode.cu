@@ -8,7 +8,9 @@
 // (sa_paged.cuh), so ragged batches, one long sequence and many short ones load
 // the GPU alike; a unit cut by the split is joined by the last of its CTAs to
 // finish.  Bound: HBM for the rows; for few of them the chain lengths, table,
-// rows, record, ticket, join.
+// rows, record, ticket, join.  Measured (bf16, 32 / 8 heads of 128): 32 x 32K
+// 671 to 698 us, 0.95 to 0.99 of the copy rate; 1 x 32K 34.5 us of which the rows
+// are 20; 1 x 2K in fp32 10.6 us.
 #include "sa_paged_decode.cuh"
 #include "sa_tc.cuh"
 
@@ -121,9 +123,8 @@ __device__ __forceinline__ bool pg_next(const PgDecodeIo& io, const PgSplit& sp,
 // What is fp32 enters as three bf16 parts of 8 bits each, cut off the top, so
 // that nothing is rounded on the way in: the weights always, and with fp32
 // caches queries, keys and values too, of whose nine products of parts all that
-// reach 2^-24 of the whole are taken.  (m16n8k16 with bf16 rows leaves the
-// tensor pipe under a fifth busy at HBM speed, the parts of fp32 rows under a
-// half; tcgen05 would want the eight query rows padded to 64 or 128.)  With up
+// reach 2^-24 of the whole are taken.  (Either way the tensor pipe is under a
+// fifth busy, so mma.sync will do.)  With up
 // to four heads rows 4..7 repeat rows 0..3 and two of the weights' parts share
 // one instruction.  The maximum is moved only when a logit passes it by 8 (2^8
 // in the sums): one vote per step.
