@@ -101,6 +101,26 @@ __device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, 
     const int cols = gh * (D / 4);
     const int parts = max(1, NT / cols), part = threadIdx.x / cols;        // part >= parts: none
     const int each = (n + parts - 1) / parts;
+    // a thread's column and records in pass c0 over the columns; the first ones
+    // are on their way before the weights are known
+    int h, e, s0, s1;
+    bool mine;
+    float4 a[kPgJoin];
+    auto place = [&](int c0) {
+        const int col = parts > 1 ? threadIdx.x % cols : c0 + threadIdx.x;
+        h = col / (D / 4);
+        e = (col % (D / 4)) * 4;
+        s0 = parts > 1 ? part * each : 0;
+        s1 = min(n, s0 + each);
+        mine = col < cols && (parts == 1 || part < parts);
+    };
+    auto load = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < kPgJoin; ++j)
+            if (mine && s + j < s1) a[j] = __ldcg(reinterpret_cast<const float4*>(rec(s + j) - h0 + 2 * hu + (h0 + h) * D + e));
+    };
+    place(0);
+    load(s0);
 #pragma unroll 1
     for (int x = warp; x < gh; x += NT / 32) {
         // the first 32 records' m and l at once
@@ -139,17 +159,14 @@ __device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, 
     __syncthreads();
 #pragma unroll 1
     for (int c0 = 0; c0 < cols; c0 += NT) {
-        const int col = parts > 1 ? threadIdx.x % cols : c0 + threadIdx.x;
-        const int h = col / (D / 4), e = (col % (D / 4)) * 4;
-        const int s0 = parts > 1 ? part * each : 0, s1 = min(n, s0 + each);
-        const bool mine = col < cols && (parts == 1 || part < parts);
+        if (c0 > 0) {
+            place(c0);
+            load(s0);
+        }
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int s = s0; mine && s < s1; s += kPgJoin) {
-            float4 a[kPgJoin];
-#pragma unroll
-            for (int j = 0; j < kPgJoin; ++j)
-                if (s + j < s1) a[j] = __ldcg(reinterpret_cast<const float4*>(rec(s + j) - h0 + 2 * hu + (h0 + h) * D + e));
+            if (s > s0) load(s);
 #pragma unroll
             for (int j = 0; j < kPgJoin; ++j) {
                 if (s + j < s1) {
@@ -166,7 +183,7 @@ __device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, 
             if (mine) sums[threadIdx.x] = A;
             __syncthreads();
             for (int p = 1; part == 0 && p < parts; ++p) {
-                const float4 B = sums[p * cols + col];
+                const float4 B = sums[p * cols + threadIdx.x];
                 A.x += B.x; A.y += B.y; A.z += B.z; A.w += B.w;
             }
         }

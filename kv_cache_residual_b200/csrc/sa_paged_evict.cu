@@ -13,7 +13,8 @@
 // which the cluster reads 64 coarse sums and then the 32 bins of one of them
 // through distributed shared memory.  Ranks by ballots and prefix sums in slot
 // order; out come the lists of freed and of late kept slots.  Bound: the chain
-// of barriers and the latency of the weights.
+// of barriers and the latency of the weights (4112 slots of 256 units: 13 us; 32K
+// of 64: 20 us; 128K of 8: 25 us, and 27 with clusters of sixteen).
 // k_evict_move: the rows, split evenly over the GPU whatever the units'
 // counts.  Bound: HBM, each moved row read once and written once (402 MB in 66 us,
 // 0.95 of the copy rate).
