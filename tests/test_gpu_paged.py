@@ -725,3 +725,24 @@ def test_threads_on_one_stream():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("G", [1, 4, 7, 8, 12, 20])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_decode_many_short_units(G, dtype, d):
+    """More short units than there are SMs."""
+    r = np.random.default_rng(90)
+    c = Case([int(x) for x in r.integers(0, 260, 110)], Hkv=4, G=G, d=d, dtype=dtype, page=24, seed=90)
+    _decode(c, weights=True, softcap=5.0)
+    out, lse = _decode(c)
+    again = sa.paged_decode(c.q, c.cache())
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("tracked", [False, True])
+def test_decode_many_short_units_masked(tracked):
+    r = np.random.default_rng(91)
+    c = Case([int(x) for x in r.integers(0, 200, 200)], Hkv=2, G=4, d=128, tracked=tracked, seed=91)
+    c.table[3, 0], c.table[5, 1] = -1, c.n_pages
+    slopes = torch.exp2(-torch.arange(1, c.Hq + 1, device=_dev(), dtype=F32))
+    _decode(c, weights=True, sink=5, local=40, slopes=slopes)
