@@ -11,10 +11,10 @@
 // may stay in place.  Then radix digits of 11, 11 and 10 bits until the digits'
 // prefix alone tells who stays (22 bits mostly do): a histogram per CTA, of
 // which the cluster reads 64 coarse sums and then the 32 bins of one of them
-// through distributed shared memory.  Ranks by ballots and prefix sums in slot
-// order; out come the lists of freed and of late kept slots.  Bound: the chain
-// of barriers and the latency of the weights (4112 slots of 256 units: 13 us; 32K
-// of 64: 20 us; 128K of 8: 25 us, and 27 with clusters of sixteen).
+// through distributed shared memory.  Ranks by prefix sums in slot order; out
+// come the lists of freed and of late kept slots.  Bound: the chain of barriers
+// and the latency of the weights (4112 slots of 256 units: 13 us; 32K of 64: 20
+// us; 128K of 8: 24 us, and 27 with clusters of sixteen).
 // k_evict_move: the rows, split evenly over the GPU whatever the units'
 // counts.  Bound: HBM, each moved row read once and written once (402 MB in 66 us,
 // 0.95 of the copy rate).
@@ -265,17 +265,27 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     // Kept before slot s: those with a larger key, and of the equal ones the first
     // `need`, so prefix counts of both kinds give every slot's place: a freed slot
     // s < keep is number s - kept(s), a late kept one number kept(s) - kept(keep).
-    // warp w takes a run of the slice, 32 slots at a time
-    const int run = ((hi - lo + kW - 1) / kW + 31) & ~31;
+    // warp w takes a run of the slice, 128 slots at a time, four in a row a lane
+    const int run = ((hi - lo + kW - 1) / kW + 127) & ~127;
     const int w0 = min(hi, lo + warp * run), w1 = min(hi, w0 + run);
+    auto quad = [&](int s0, uint32_t (&k)[4]) {        // masked keys; past the run 0, below every prefix
+        const int s = s0 + 4 * lane;
+        const uint4 y = s < w1 ? *reinterpret_cast<const uint4*>(keys + s - lo) : make_uint4(0u, 0u, 0u, 0u);
+        k[0] = y.x & mask; k[1] = y.y & mask; k[2] = y.z & mask; k[3] = y.w & mask;
+    };
     uint32_t n[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 4
-    for (int s = w0 + lane; s < w1; s += 32) {
-        const uint32_t k = keys[s - lo] & mask;
-        n[0] += k > prefix ? 1u : 0u;
-        n[1] += k == prefix ? 1u : 0u;
-        n[2] += k > prefix && s < keep ? 1u : 0u;
-        n[3] += k == prefix && s < keep ? 1u : 0u;
+#pragma unroll 2
+    for (int s0 = w0; s0 < w1; s0 += 128) {
+        uint32_t k[4];
+        quad(s0, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool early = s0 + 4 * lane + i < keep;
+            n[0] += k[i] > prefix ? 1u : 0u;
+            n[1] += k[i] == prefix ? 1u : 0u;
+            n[2] += k[i] > prefix && early ? 1u : 0u;
+            n[3] += k[i] == prefix && early ? 1u : 0u;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
@@ -304,19 +314,33 @@ k_evict_select(PagedEvictArgs a, int moves, int32_t* lists, int32_t* counts, uin
     if (threadIdx.x == 0 && rank == 0) counts[u] = keep - (int32_t)kept1;
     int32_t* holes = lists + (size_t)u * 2 * moves;
     int32_t* lates = holes + moves;
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int s0 = w0; s0 < w1; s0 += 32) {
-        const int s = s0 + lane;
-        const uint32_t k = s < w1 ? keys[s - lo] & mask : 0u;
-        const bool above = s < w1 && k > prefix, tie = s < w1 && k == prefix;
-        const unsigned mg = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, tie);
-        const uint32_t ties = eq + __popc(me & below), kept = gt + __popc(mg & below) + min(need, ties);
-        const bool stays = above || (tie && ties < need);
-        if (s < keep && s < w1 && !stays) holes[s - (int)kept] = s;
-        if (s >= keep && stays) lates[kept - kept1] = s;
-        gt += __popc(mg);
-        eq += __popc(me);
+#pragma unroll 1
+    for (int s0 = w0; s0 < w1; s0 += 128) {
+        uint32_t k[4], own = 0u;                       // larger keys in the low half, ties in the high one
+        quad(s0, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own += k[i] > prefix ? 1u : k[i] == prefix ? 0x10000u : 0u;
+        uint32_t inc = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        uint32_t g = gt + ((inc - own) & 0xffffu), ties = eq + ((inc - own) >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + 4 * lane + i;
+            const bool above = k[i] > prefix, tie = k[i] == prefix;
+            const bool stays = above || (tie && ties < need);
+            const uint32_t kept = g + min(need, ties);
+            if (s < keep && s < w1 && !stays) holes[s - (int)kept] = s;
+            if (s >= keep && stays) lates[kept - kept1] = s;
+            g += above ? 1u : 0u;
+            ties += tie ? 1u : 0u;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+        gt += all & 0xffffu;
+        eq += all >> 16;
     }
     if constexpr (CL > 1) ev_sync<CL>();               // no CTA leaves while another reads its memory
 }
