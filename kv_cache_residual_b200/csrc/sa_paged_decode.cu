@@ -139,7 +139,9 @@ struct PgTc {
     // dims of row r (K), of rows 2t, 2t+1, .. (V)
     static constexpr int kPitchK = kBf16 ? 2 * D + 16 : 4 * D + 64, kPitchV = kBf16 ? 2 * D + 16 : 4 * D + 16;
     static constexpr int kV = 16 * kPitchK, kDist = kV + 16 * kPitchV, kBytes = kDist + 16 * 4;
-    static constexpr int kStages = !kBf16 ? 2 : D == 128 ? 3 : 5;        // with the scratch, what an SM has room for
+    // one stage ahead of the one at hand is enough with eight warps (32 x 32K 688
+    // us, 702 with two ahead, four warps and more stages 830 and up)
+    static constexpr int kStages = !kBf16 || D == 128 ? 2 : 4;
     static constexpr int kRing = kWarps * kStages * kBytes;
     static constexpr int kAcc = kWarps * 4 * (D + 4);            // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
