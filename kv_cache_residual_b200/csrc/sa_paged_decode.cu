@@ -9,8 +9,8 @@
 // the GPU alike; a unit cut by the split is joined by the last of its CTAs to
 // finish.  Bound: HBM for the rows; for few of them the chain lengths, table,
 // rows, record, ticket, join.  Measured (bf16, 32 / 8 heads of 128): 32 x 32K
-// 671 to 698 us, 0.95 to 0.99 of the copy rate; 1 x 32K 34.5 us of which the rows
-// are 20; 1 x 2K in fp32 10.6 us.
+// 690 to 719 us, 0.92 to 0.96 of the copy rate; 1 x 32K 34.5 us of which the rows
+// are 20; 1 x 2K in fp32 10.5 us.
 #include "sa_paged_decode.cuh"
 #include "sa_tc.cuh"
 
