@@ -69,7 +69,9 @@ inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
     p.extra = paged_extra(d);
     p.ldx = (d.cap + kPgTile - 1) / kPgTile * kPgTile;
     size_t off = 0;
-    p.off_cnt = off; off = align256(off + sizeof(unsigned) * (size_t)d.U() * d.nhb);
+    // a ticket per eight heads whatever the type's units hold, so that the bytes
+    // to be zeroed, and where the records begin, follow from B, Hq and Hkv alone
+    p.off_cnt = off; off = align256(off + sizeof(unsigned) * (size_t)d.U() * ((d.G + 7) / 8));
     p.off_rec = off; off = align256(off + sizeof(float) * 2 * (size_t)p.grid * p.rec);
     // with weights: log2 of every row's mass, and the logits (log2) of its slots
     p.off_lse = off; if (weights) off = align256(off + sizeof(float) * (size_t)d.B * d.Hq);

@@ -746,3 +746,18 @@ def test_decode_many_short_units_masked(tracked):
     c.table[3, 0], c.table[5, 1] = -1, c.n_pages
     slopes = torch.exp2(-torch.arange(1, c.Hq + 1, device=_dev(), dtype=F32))
     _decode(c, weights=True, sink=5, local=40, slopes=slopes)
+
+
+def test_decode_scratch_of_two_types():
+    """Wide groups in bf16, then in fp32, on one stream: as many bytes of scratch
+    and tickets, not as many heads in a record."""
+    r = np.random.default_rng(100)
+    cases = [Case([3000] * 16 + [1] * 576, Hkv=8, G=16, d=64, seed=101),          # long units: records of the first CTAs
+             Case([int(x) for x in r.integers(1, 193, 592)], Hkv=8, G=16, dtype=F32, cols=12, seed=102)]
+    for _ in range(2):
+        for c in cases:
+            out = torch.full((c.B, c.Hq, c.d), 7.0, device=_dev())
+            lse = torch.full((c.B, c.Hq), 7.0, device=_dev())
+            sa.paged_decode(c.q, c.cache(), out=out, lse=lse)
+            torch.cuda.synchronize()
+            _check_decode(c, out, lse)

@@ -177,3 +177,18 @@ def test_factors_that_overflow_are_refused():
 
 def test_evict_refuses_to_write_over_seen():
     assert _evict(cache=_cache(pos=0x30000, seen=0x20000)) == sa.SA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("G", [1, 8, 9, 10, 16, 17, 32])
+@pytest.mark.parametrize("dtype,d", [(sa.SA_BF16, 64), (sa.SA_BF16, 128), (sa.SA_F32, 64), (sa.SA_F32, 128)])
+def test_decode_scratch_has_the_tickets_before_the_records(G, dtype, d):
+    """The tickets of every type take the bytes the header names, so that two
+    shapes with as many of them have no record where the other has a ticket."""
+    for B in (1, 148, 592):
+        sh = _shape(B=B, Hq=8 * G, Hkv=8, d=d, dtype=dtype)
+        hu = 16 if dtype == sa.SA_BF16 and G > 8 else 8                # heads of a record
+        units = B * 8 * -(-G // hu)
+        records = 4 * 2 * min(148, units * 5) * hu * (2 + d)           # 320 slots are 5 tiles
+        tickets = 4 * B * 8 * -(-G // 8)
+        n = sa._lib().sa_paged_workspace_size(ctypes.byref(sh), sa.OP_PAGED_DECODE, 0)
+        assert n == -(-tickets // 256) * 256 + -(-records // 256) * 256
