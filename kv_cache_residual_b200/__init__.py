@@ -518,7 +518,8 @@ class PagedCache:
 
     The object holds the tensors and reads nothing from them: their values may
     change between calls, and between replays of a captured one.  Other tensors
-    make another cache."""
+    make another cache.  The calls' scratch belongs to their stream, not to the
+    cache: as much as the largest call on it took."""
 
     def __init__(self, k, v, table, lengths, pos=None, seen=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device and k.is_cuda,
@@ -529,7 +530,7 @@ class PagedCache:
         self.capacity = self.max_pages * self.page
         self.dtype, self.device = k.dtype, k.device
         self.slots = torch.Size((self.B, self.Hkv, self.capacity))      # of pos and of the weights
-        self._ws = {}
+        self._plans = {}
         self._tensors = k, v, table, lengths, pos, seen
         strides = []
         for t in (k, v):
@@ -601,39 +602,49 @@ def _here(device, stream):
     return None
 
 
-_PAGED_WS = {}
+_PAGED_WS = {}                      # (device index, stream): (tensor, its zeroed bytes, the bytes after them, their address)
 _PAGED_LOCK = threading.Lock()      # a call's kernels follow one another on its stream, whoever else calls
 
 
+def _stream_scratch(device, stream, tickets, rest):
+    """The address of `tickets` zero bytes and then `rest` bytes, multiples of
+    256: one buffer per stream, replaced where a call needs more than any before
+    it, so that a stream keeps what its largest call takes.  Zero bytes end where
+    the others begin, whatever their number: no call writes to another's tickets,
+    and every call leaves its own zero."""
+    key = (device.index, stream)
+    kept = _PAGED_WS.get(key)
+    if kept is None or tickets > kept[1] or rest > kept[2]:
+        zeros, size = (tickets, rest) if kept is None else (max(tickets, kept[1]), max(rest, kept[2]))
+        # the old buffer goes first; what still runs on it is before the new one's first use on this stream
+        kept = None
+        _PAGED_WS.pop(key, None)
+        t = torch.empty(zeros + size, dtype=torch.uint8, device=device)
+        t[:zeros].zero_()
+        kept = _PAGED_WS[key] = (t, zeros, size, t.data_ptr() + zeros)
+    return kept[3] - tickets
+
+
 def _paged_workspace(cache, Hq, op, arg, stream):
-    """Scratch of a paged call with its tickets zeroed, kept per (device, stream,
-    op, size, tickets): calls on one stream follow one another, calls on two
-    never share it.  A call that is being captured gets its own, whose tickets
-    the graph zeroes at each replay, so that graphs replayed side by side do not
-    share it either."""
-    capturing = torch._C._cuda_isCurrentStreamCapturing()
-    if not capturing:
-        ws = cache._ws.get((op, arg, Hq, stream))
-        if ws is not None:
-            return ws
-    shape = cache._for_heads(Hq)
-    n = _lib().sa_paged_workspace_size(ctypes.byref(shape), op, arg)
-    if n == 0:
-        raise SAError(SA_ERR_INVALID_ARG, "sa_paged_workspace_size")
-    # two shapes of one size can have their records where the other has tickets
-    tickets = 4 * cache.B * cache.Hkv * -(-Hq // (8 * cache.Hkv)) if op == OP_PAGED_DECODE else 0
-    key = (cache.device.index, stream, op, n, tickets)
-    t = None if capturing else _PAGED_WS.get(key)
-    if t is None:
+    """(C shape, address, bytes, tensor to keep or None) of a paged call's scratch.
+    Calls on one stream follow one another and share it, calls on two never do.
+    A call that is being captured gets its own, whose tickets the graph zeroes at
+    each replay, so that graphs replayed side by side do not share it either."""
+    plan = cache._plans.get((op, arg, Hq))
+    if plan is None:
+        shape = cache._for_heads(Hq)
+        n = _lib().sa_paged_workspace_size(ctypes.byref(shape), op, arg)
+        if n == 0:
+            raise SAError(SA_ERR_INVALID_ARG, "sa_paged_workspace_size")
+        tickets = 4 * cache.B * cache.Hkv * -(-Hq // (8 * cache.Hkv)) if op == OP_PAGED_DECODE else 0
+        plan = cache._plans[(op, arg, Hq)] = (ctypes.byref(shape), n, -(-tickets // 256) * 256)
+    shape, n, tickets = plan
+    if torch._C._cuda_isCurrentStreamCapturing():
         t = torch.empty(n, dtype=torch.uint8, device=cache.device)
         if tickets:
             t[:tickets].zero_()
-        if not capturing:
-            _PAGED_WS[key] = t
-    ws = (shape, ctypes.byref(shape), t.data_ptr(), n, t)
-    if not capturing:
-        cache._ws[(op, arg, Hq, stream)] = ws
-    return ws
+        return shape, t.data_ptr(), n, t
+    return shape, _stream_scratch(cache.device, stream, tickets, n - tickets), n, None
 
 
 def paged_append(cache, k_new, v_new, start=None, weight=None, stream=None):
@@ -682,7 +693,7 @@ def _decode(s, cache, q, p, Hq, weights, out, lse):
     pl = _dense(lse, "lse", torch.float32, shape[:2], cache.device)
     with _PAGED_LOCK:
         ws = _paged_workspace(cache, Hq, OP_PAGED_DECODE, weights, s)
-        status = _lib().sa_paged_decode(ws[1], cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl, ws[2], ws[3], s)
+        status = _lib().sa_paged_decode(ws[0], cache._byref[1], ctypes.byref(p), q.data_ptr(), po, pl, ws[1], ws[2], s)
     if status != SA_OK:
         _check(status, "sa_paged_decode")
     return out, lse
@@ -736,7 +747,7 @@ def _evict(s, cache, weight, budget, sink, local, lengths_out, weight_out, pos_o
           _dense(pos_out, "pos_out", torch.int32, slots, dev))
     with _PAGED_LOCK:
         ws = _paged_workspace(cache, cache.Hkv, OP_PAGED_EVICT, budget, s)
-        status = _lib().sa_paged_evict(*cache._byref, weight, budget, sink, local, *po, ws[2], ws[3], s)
+        status = _lib().sa_paged_evict(*cache._byref, weight, budget, sink, local, *po, ws[1], ws[2], s)
     if status != SA_OK:
         _check(status, "sa_paged_evict")
     return lengths_out, weight_out, pos_out

@@ -761,3 +761,30 @@ def test_decode_scratch_of_two_types():
             sa.paged_decode(c.q, c.cache(), out=out, lse=lse)
             torch.cuda.synchronize()
             _check_decode(c, out, lse)
+
+
+def test_scratch_is_kept_by_stream_not_by_shape():
+    """A table that grows and a batch that grows, with weights: what stays
+    allocated is the scratch of the largest call, not of all."""
+    dev = _dev()
+    stream = torch.cuda.Stream()
+    c = Case([40, 9, 300, 7, 64, 1, 200, 90], G=8, d=64, cols=64, seed=110)
+    k, v = c.k, c.v
+
+    def call(B, cols):
+        table = torch.from_numpy(c.table_h[:B, :cols].copy()).to(dev)
+        cache = sa.PagedCache(k, v, table, c.lengths[:B])
+        wo = torch.zeros(cache.slots, device=dev)
+        sa.paged_decode(c.q[:B], cache, weight_out=wo, stream=stream)
+        sa.paged_evict(cache, wo, 16, 2, 2, stream=stream)
+        torch.cuda.synchronize()
+
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    call(8, 64)
+    most = torch.cuda.memory_allocated() - before
+    for B in range(1, 9):
+        for cols in range(1, 65, 3):
+            call(B, cols)
+    assert torch.cuda.memory_allocated() - before <= most
+    assert most < 2 ** 22

@@ -192,3 +192,25 @@ def test_decode_scratch_has_the_tickets_before_the_records(G, dtype, d):
         tickets = 4 * B * 8 * -(-G // 8)
         n = sa._lib().sa_paged_workspace_size(ctypes.byref(sh), sa.OP_PAGED_DECODE, 0)
         assert n == -(-tickets // 256) * 256 + -(-records // 256) * 256
+
+
+def test_scratch_of_a_stream_is_its_largest_calls(monkeypatch):
+    """Calls of many sizes on one stream keep one buffer, with zeros before the
+    place where every call writes."""
+    import torch
+    monkeypatch.setattr(sa, "_PAGED_WS", {})
+    r = np.random.default_rng(5)
+    cpu, most = torch.device("cpu"), [0, 0]
+    for _ in range(200):
+        tickets, rest = 256 * int(r.integers(0, 40)), 256 * int(r.integers(1, 4000))
+        most = [max(most[0], tickets), max(most[1], rest)]
+        at = sa._stream_scratch(cpu, 7, tickets, rest)
+        assert sa._stream_scratch(cpu, 7, tickets, rest) == at          # kept
+        assert list(sa._PAGED_WS) == [(None, 7)]
+        t = sa._PAGED_WS[(None, 7)][0]
+        assert t.numel() == sum(most)
+        first = at - t.data_ptr()
+        assert first >= 0 and not t[first:first + tickets].any() and first + tickets + rest <= t.numel()
+        t[first + tickets:first + tickets + rest] = 1                   # as a call leaves it
+    other = sa._stream_scratch(cpu, 8, 0, 256)
+    assert len(sa._PAGED_WS) == 2 and other == sa._PAGED_WS[(None, 8)][0].data_ptr()
