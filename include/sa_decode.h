@@ -459,6 +459,10 @@ SA_API sa_status sa_dense_decode(const sa_shape* shape, const void* q, const voi
  * token a slot holds.  Lengths, tables and positions are read on the device
  * by each call, so a call captured in a CUDA graph follows them at replay; they
  * must not be written while a call runs.
+ * What a call writes lies apart from what it reads and from its other outputs;
+ * one whose arrays overlap is refused (the pools, which are strided, are not
+ * looked at).  Two may be the same: weight_out and weight, and, in fp32 with
+ * dense queries, out and q.
  * The method has no counterpart: these are the dense operators a serving
  * program needs beside the sparse ones.
  *
@@ -569,7 +573,7 @@ SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cac
  * every sequence: lengths_out [B] = min(lengths[b], budget), and for slots s <
  * lengths_out[b] the weights and positions of the tokens now there
  * (weight_out f32, pos_out int32, both [B, Hkv, ldw]; past it they are left as
- * they were).  The outputs are other arrays than the inputs: repeating a call
+ * they were).  The outputs lie apart from the inputs: repeating a call
  * on the same inputs gives the same result.  A sequence's pages must be its
  * own, each in one place of the table: rows are moved in place.  Pass the
  * outputs as the cache's lengths, pos and weights from then on. */

@@ -54,6 +54,21 @@ bool check_cache(const sa_paged_cache* c) {
     return c->pos == nullptr || (aligned4(c->pos) && aligned4(c->seen));
 }
 
+// whether what a call writes lies apart from what it reads and from its other outputs
+bool apart(const Span* out, int n_out, const Span* in, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return false;
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(out[i], in[j])) return false;
+    }
+    return true;
+}
+
+Span table_span(const PagedDims& d, const sa_paged_cache& c) { return Span(c.table, 4LL * d.B * d.max_pages); }
+Span per_slot(const PagedDims& d, const void* p) { return Span(p, 4LL * d.cap, d.U(), 4LL * d.ldw); }
+Span per_sequence(const PagedDims& d, const void* p) { return Span(p, 4LL * d.B); }
+
 bool strides_ok(long long x, const PagedDims& d) { return x >= 1 && x % (16 / d.esz()) == 0; }
 
 }  // namespace
@@ -86,6 +101,10 @@ sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cache* cac
         token_stride = (long long)d.Hkv * d.d;
     }
     if (!strides_ok(token_stride, d) || !strides_ok(head_stride, d)) return SA_ERR_INVALID_ARG;
+    const Span out[] = {per_slot(d, cache->pos), per_slot(d, weight)};
+    const Span in[] = {table_span(d, *cache), per_sequence(d, cache->lengths), per_sequence(d, cache->seen),
+                       Span(start, 4LL * (d.B + 1))};
+    if (!apart(out, 2, in, 4)) return SA_ERR_INVALID_ARG;
     const PagedAppendArgs a{paged_view(d, *cache), k_new, v_new, token_stride, head_stride, start, n_new,
                             cache->pos, weight};
     return launch_paged_append(d, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
@@ -114,6 +133,14 @@ sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cac
     if (!strides_ok(qs, d)) return SA_ERR_INVALID_ARG;
     const PagedDecodePlan plan = paged_decode_plan(d, p.weight_out != nullptr);
     if (ws == nullptr || ws_bytes < plan.bytes || !aligned16(ws)) return SA_ERR_WORKSPACE;
+    // in place: weights at the very slots, and queries that are exactly the rows written
+    const bool same_w = p.weight == p.weight_out, same_q = q == out && !d.bf16 && qs == (long long)d.Hq * d.d;
+    const Span outs[] = {Span(out, 4LL * d.B * d.Hq * d.d), Span(lse, 4LL * d.B * d.Hq), per_slot(d, p.weight_out),
+                         Span(ws, (long long)plan.bytes)};
+    const Span ins[] = {Span(same_q ? nullptr : q, (long long)d.Hq * d.d * d.esz(), d.B, qs * d.esz()),
+                        table_span(d, *cache), per_sequence(d, cache->lengths), per_sequence(d, cache->seen),
+                        per_slot(d, cache->pos), Span(p.slopes, 4LL * d.Hq), per_slot(d, same_w ? nullptr : p.weight)};
+    if (!apart(outs, 4, ins, 7)) return SA_ERR_INVALID_ARG;
     const PagedDecodeArgs a{paged_view(d, *cache), q, qs, p.slopes, p.weight, p.weight_out, out, lse,
                             scale, p.softcap, p.sink, p.local, static_cast<char*>(ws)};
     return launch_paged_decode(d, plan, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
@@ -130,9 +157,13 @@ sa_status sa_paged_evict(const sa_paged_shape* shape, const sa_paged_cache* cach
         !aligned4(pos_out))
         return SA_ERR_INVALID_ARG;
     if (budget < 1 || sink < 0 || local < 0 || (long long)sink + local > budget) return SA_ERR_INVALID_ARG;
-    if (lengths_out == cache->lengths || lengths_out == cache->seen || weight_out == weight || pos_out == cache->pos) return SA_ERR_INVALID_ARG;
     const PagedEvictPlan plan = paged_evict_plan(d, budget);
     if (ws == nullptr || ws_bytes < plan.bytes || !aligned16(ws)) return SA_ERR_WORKSPACE;
+    const Span out[] = {per_sequence(d, lengths_out), per_slot(d, weight_out), per_slot(d, pos_out),
+                        Span(ws, (long long)plan.bytes)};
+    const Span in[] = {table_span(d, *cache), per_sequence(d, cache->lengths), per_sequence(d, cache->seen),
+                       per_slot(d, cache->pos), per_slot(d, weight)};
+    if (!apart(out, 4, in, 5)) return SA_ERR_INVALID_ARG;
     const PagedEvictArgs a{paged_view(d, *cache), weight, budget, sink, local, lengths_out, weight_out, pos_out,
                            static_cast<char*>(ws)};
     return launch_paged_evict(d, plan, a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;

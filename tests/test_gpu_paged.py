@@ -788,3 +788,40 @@ def test_scratch_is_kept_by_stream_not_by_shape():
             call(B, cols)
     assert torch.cuda.memory_allocated() - before <= most
     assert most < 2 ** 22
+
+
+def test_outputs_beside_inputs():
+    """Arrays that touch one another in one buffer, and fp32 queries that become
+    the output; one element further in is refused."""
+    dev = _dev()
+    c = Case([300, 0, 17, 64], dtype=F32, tracked=True, seed=120)
+    n = c.weight.numel()
+    buf = torch.zeros(3 * n + 8, device=dev)
+    w, wo = buf[:n].view(c.weight.shape), buf[n:2 * n].view(c.weight.shape)
+    w.copy_(c.weight)
+    cache = c.cache()
+    out, lse = sa.paged_decode(c.q, cache, weight=w, weight_out=wo)
+    _check_decode(c, out, lse, wo, c.weight, wo)
+    with pytest.raises(sa.SAError):
+        sa.paged_decode(c.q, cache, weight=w, weight_out=buf[n - 1:2 * n - 1].view(c.weight.shape))
+    mine = c.q.clone()
+    o, l = sa.paged_decode(mine, cache, out=mine)
+    assert o is mine and torch.equal(o, out) and torch.equal(l, lse)
+    fused = torch.randn(c.B, c.Hq + 2, c.d, device=dev)
+    fused[:, :c.Hq] = c.q
+    rows = fused.view(-1)[:c.B * c.Hq * c.d].view(c.B, c.Hq, c.d)
+    with pytest.raises(sa.SAError):
+        sa.paged_decode(fused[:, :c.Hq], cache, out=rows)
+    # a sum row of every sequence between its queries and the next one's
+    lse2 = fused.view(c.B, -1)[1, c.Hq * c.d:][:c.B * c.Hq].view(c.B, c.Hq)
+    o, l = sa.paged_decode(fused[:, :c.Hq], cache, lse=lse2)
+    assert torch.equal(o, out) and torch.equal(l, lse)
+    with pytest.raises(sa.SAError):
+        sa.paged_evict(cache, w, 32, 2, 2, weight_out=buf[1:n + 1].view(c.weight.shape))
+    ints = torch.zeros(n + 4, dtype=I32, device=dev)
+    with pytest.raises(sa.SAError):
+        sa.paged_evict(cache, w, 32, 2, 2, pos_out=ints[:n].view(c.weight.shape), lengths_out=ints[n - 4:n])
+    c.weight.copy_(w)
+    kept, w2, p2 = sa.paged_evict(cache, w, 32, 2, 2, weight_out=buf[n:2 * n].view(c.weight.shape),
+                                  pos_out=ints[:n].view(c.weight.shape), lengths_out=ints[n:])
+    assert kept.tolist() == [min(x, 32) for x in c.lens]

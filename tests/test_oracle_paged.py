@@ -214,3 +214,39 @@ def test_scratch_of_a_stream_is_its_largest_calls(monkeypatch):
         t[first + tickets:first + tickets + rest] = 1                   # as a call leaves it
     other = sa._stream_scratch(cpu, 8, 0, 256)
     assert len(sa._PAGED_WS) == 2 and other == sa._PAGED_WS[(None, 8)][0].data_ptr()
+
+
+FAR = [0x1000000 * i for i in range(1, 12)]           # addresses apart from one another
+
+
+def test_outputs_that_overlap_are_refused():
+    """The shape's per-slot arrays take 5120 bytes, out 8192, lse 64, queries 4096."""
+    bad = sa.SA_ERR_INVALID_ARG
+    k, v, table, lengths, pos, seen, a, b, c, d, ws = FAR
+    cache = _cache(k=k, v=v, table=table, lengths=lengths, pos=pos, seen=seen)
+    for kw in (dict(weight_out=a + 5116), dict(weight_out=a - 5116), dict(pos_out=a + 4), dict(pos_out=pos + 5116),
+               dict(weight_out=pos - 5116), dict(lengths_out=a + 5116), dict(lengths_out=lengths + 4),
+               dict(lengths_out=seen - 4), dict(lengths_out=table + 156), dict(weight_out=table - 4000),
+               dict(pos_out=b + 64), dict(lengths_out=b + 5116), dict(lengths_out=c), dict(ws=a + 4096), dict(ws=b - 16)):
+        args = dict(weight=a, weight_out=b, pos_out=c, lengths_out=d, ws=ws)
+        args.update(kw)
+        assert _evict(cache=cache, **args) == bad, kw
+    for kw in (dict(weight_out=a + 5116), dict(weight_out=a + 4), dict(weight_out=pos + 16), dict(weight_out=b + 8188),
+               dict(weight_out=b - 5116), dict(weight_out=c + 60), dict(weight_out=lengths - 5116), dict(slopes=b + 4),
+               dict(weight_out=d + 4092), dict(slopes=c + 60)):
+        args = dict(weight=a, weight_out=FAR[10] + 0x1000000)
+        args.update(kw)
+        assert _decode(cache=cache, params=_params(**args), q=d, out=b, lse=c, ws=ws) == bad, kw
+    for kw in (dict(out=d), dict(out=d + 4080), dict(lse=d + 4092), dict(lse=b + 8188), dict(ws=b + 16), dict(ws=d + 16),
+               dict(out=table - 16), dict(lse=lengths), dict(lse=seen + 4)):
+        args = dict(q=d, out=b, lse=c, ws=ws)
+        args.update(kw)
+        assert _decode(cache=cache, **args) == bad, kw
+    # fp32 queries in the place of the output, but not its rows
+    f32 = _shape(dtype=sa.SA_F32)
+    assert _decode(shape=f32, cache=cache, q=b + 16, out=b, lse=c, ws=ws) == bad
+    assert _decode(shape=f32, cache=cache, q=b, out=b, lse=c, ws=ws, params=_params(q_stride=2048)) == bad
+    for kw in (dict(weight=pos + 4), dict(weight=table), dict(weight=lengths - 4), dict(weight=seen - 5116),
+               dict(weight=a, start=a + 5116, n=5)):
+        assert _append(cache=cache, **kw) == bad, kw
+    assert _append(cache=cache, start=pos + 8, n=5) == bad
