@@ -504,7 +504,8 @@ typedef struct {
 } sa_paged_cache;
 
 /*   scale       softmax scale (0 = 1/sqrt(d))
- *   softcap     c > 0: logits capped to c tanh(scale q.k / c); 0: not capped
+ *   softcap     c > 0: logits capped to c tanh(scale q.k / c) (scale / c has to
+ *               be a normal fp32 number); 0: not capped
  *   sink, local with local > 0 a slot is visible when its position is one of
  *               the first `sink` or the last `local` (position > newest -
  *               local); local = 0: every slot

@@ -1,6 +1,8 @@
 // C entry points of the paged cache (declared in include/sa_decode.h):
 // argument checks, workspace sizing and dispatch.  Every check runs before
 // anything is enqueued, so a rejected call leaves the stream untouched.
+#include <float.h>
+
 #include "sa_check.h"
 #include "sa_paged.h"
 
@@ -125,9 +127,9 @@ sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cac
         (p.weight != nullptr && (!aligned4(p.weight) || p.weight_out == nullptr)) ||
         (p.weight_out != nullptr && !aligned4(p.weight_out)))
         return SA_ERR_INVALID_ARG;
-    // what the kernel multiplies by has to be a number
-    const float scale = resolve_scale(p.scale, d.d);
-    if (!(scale * 1.5f < INFINITY) || (p.softcap > 0.f && !(scale / p.softcap < INFINITY && p.softcap * 1.5f < INFINITY)))
+    // what the kernel multiplies by has to be a number, and a quotient one of full precision
+    const float scale = resolve_scale(p.scale, d.d), cap_in = p.softcap > 0.f ? scale / p.softcap : 1.f;
+    if (!(scale * 1.5f < INFINITY) || !(p.softcap * 1.5f < INFINITY) || !(cap_in >= FLT_MIN && cap_in < INFINITY))
         return SA_ERR_INVALID_ARG;
     const long long qs = p.q_stride == 0 ? (long long)d.Hq * d.d : p.q_stride;
     if (!strides_ok(qs, d)) return SA_ERR_INVALID_ARG;

@@ -825,3 +825,16 @@ def test_outputs_beside_inputs():
     kept, w2, p2 = sa.paged_evict(cache, w, 32, 2, 2, weight_out=buf[n:2 * n].view(c.weight.shape),
                                   pos_out=ints[:n].view(c.weight.shape), lengths_out=ints[n:])
     assert kept.tolist() == [min(x, 32) for x in c.lens]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_caps_that_do_not_bind(dtype):
+    """A cap at the largest that is taken is no cap.  Logits here stay below 8, off
+    by 2^-150 of the cap (the quotient's subnormals: 5e-9) and 8 u of their own on
+    either side; weights are off by twice that, and values lie below 6."""
+    c = Case([700, 3], dtype=dtype, seed=130)
+    out, lse = sa.paged_decode(c.q, c.cache())
+    capped, l = sa.paged_decode(c.q, c.cache(), softcap=7.5e36)
+    off = 2 * 8 * U * 8 + 2.0 ** -150 * 7.5e36
+    assert (l - lse).abs().max() <= off + 4 * U * 16
+    assert (out - capped).abs().max() <= 2 * off * 6 + 1e-6

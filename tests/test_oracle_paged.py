@@ -250,3 +250,12 @@ def test_outputs_that_overlap_are_refused():
                dict(weight=a, start=a + 5116, n=5)):
         assert _append(cache=cache, **kw) == bad, kw
     assert _append(cache=cache, start=pos + 8, n=5) == bad
+
+
+def test_factors_that_underflow_are_refused():
+    """scale / softcap below the least normal number has too few bits to multiply by."""
+    bad = sa.SA_ERR_INVALID_ARG
+    k, v, table, lengths, pos, seen, a, b, c, d, ws = FAR
+    cache = _cache(k=k, v=v, table=table, lengths=lengths)
+    for kw in (dict(softcap=1e37), dict(scale=1e-6, softcap=1e38), dict(scale=1e-20, softcap=1e20)):
+        assert _decode(cache=cache, params=_params(**kw), q=a, out=b, lse=c, ws=ws) == bad, kw
