@@ -561,9 +561,11 @@ k_paged_decode(PgDecodeIo io) {
                     const float sc = m[k] == -INFINITY ? 0.f : ex2(m[k] - mx);
                     m[k] = mx;
                     l[k] *= sc;
+                    // none so far but -inf, or what is not a number and has to stay that
+                    const float to = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        p[k][j] = dd[j] == INFINITY || mx == -INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j], mx);
+                        p[k][j] = dd[j] == INFINITY ? -INFINITY : pg_logit(io, x[k][j], sl[k], dd[j], to);
                     const float c0 = __shfl_sync(0xffffffffu, sc, 8 * t), c1 = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {

@@ -838,3 +838,30 @@ def test_decode_caps_that_do_not_bind(dtype):
     off = 2 * 8 * U * 8 + 2.0 ** -150 * 7.5e36
     assert (l - lse).abs().max() <= off + 4 * U * 16
     assert (out - capped).abs().max() <= 2 * off * 6 + 1e-6
+
+
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 4), (BF, 64, 8), (BF, 128, 12), (F32, 128, 4), (F32, 64, 8)])
+@pytest.mark.parametrize("lens", [[200, 40], [9000, 30], [40] * 200], ids=["short", "long", "many"])
+def test_decode_queries_that_are_not_numbers(lens, dtype, d, G):
+    """A head's query with a NaN gives a row of NaN, and leaves the other heads as they are."""
+    c = Case(lens, G=G, d=d, dtype=dtype, seed=150)
+    base, lse0 = sa.paged_decode(c.q, c.cache())
+    rows = [(0, 0), (0, G), (1, 2 * G - 1), (len(lens) - 1, 1)]
+    want, wl = base.clone(), lse0.clone()
+    for b, h in rows:
+        c.q[b, h, 5] = float("nan")
+        want[b, h], wl[b, h] = float("nan"), float("nan")
+    wo = torch.zeros_like(c.weight)
+    out, lse = sa.paged_decode(c.q, c.cache(), weight_out=wo)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(torch.isnan(lse), torch.isnan(wl))
+    # the other heads' maxima move at other steps: both runs are within the bound of
+    # the module's head, for logits of sum |q k| / sqrt(d) < 16 and sums of p |v| < 4
+    rel = 8 * U * (d / 16 + 5) * 16
+    rel = 4 * rel + 2 * (24 * 1.25 * 2.0 ** -22 + (max(lens) / 8 + 64) * U)
+    assert (out - want).nan_to_num(nan=0.0).abs().max() <= 2 * rel * 4
+    assert (lse - wl).nan_to_num(nan=0.0).abs().max() <= 2 * rel
+    live = torch.arange(c.cap, device=_dev()) < c.lengths[:, None]
+    for b in range(c.B):
+        for g in range(c.Hkv):
+            bad = any(x == b and h // G == g for x, h in rows)
+            assert torch.equal(torch.isnan(wo[b, g]), live[b] & bad)
