@@ -557,9 +557,10 @@ SA_API sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cac
  * over the visible slots (out [B, Hq, d] f32, lse [B, Hq] f32 or NULL).  A
  * row that sees nothing (length 0, a window that leaves none, no valid page)
  * gives out = 0, lse = -inf and adds no weight.  q [B, Hq, d] in dtype.  Keys
- * and values of slots that are not seen are not read; of those seen, a key's
- * infinities count as the formula has them (a logit of -inf is no weight), a
- * value that is not finite gives NaN. */
+ * and values of slots that are not seen are not read; of those seen,
+ * infinities in keys and values count as the formula has them: a logit of -inf
+ * has the weight 0, and its product with an infinite value is NaN; every other
+ * weight is above 0, however small. */
 SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cache,
                                  const sa_paged_params* params, const void* q, float* out, float* lse, void* ws,
                                  size_t ws_bytes, void* stream);

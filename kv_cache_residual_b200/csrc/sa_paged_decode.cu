@@ -67,11 +67,11 @@ struct PgPart {
     float* rec;
     __device__ __forceinline__ PgPart(const PgDecodeIo& io, const PgUnit<T, D>& u)
         : whole(u.tile == 0 && u.end == u.nt), rec(pg_rec(io.rec, io.c.hu * (2 + D), blockIdx.x, u.tile == 0)) {}
-    // accumulator A of dim e of head h, mass L relative to 2^M
+    // accumulator A of dim e of head h, mass L relative to 2^M; odd: as pg_element
     __device__ __forceinline__ void put(const PgDecodeIo& io, const PgUnit<T, D>& u, int h, int e, float A, float M,
-                                        float L) const {
+                                        float L, bool& odd) const {
         if (whole) {
-            io.out[(u.qh0 + h) * D + e] = A * pg_inv(L);
+            io.out[(u.qh0 + h) * D + e] = pg_element(A, pg_inv(L), odd);
             if (e == 0) pg_write_lse(io, u.qh0 + h, M, L);
         } else {
             rec[2 * io.c.hu + h * D + e] = A;
@@ -80,21 +80,81 @@ struct PgPart {
     }
 };
 
-// after all have put: the unit's last CTA joins.  All threads call; f as pg_join.
+// The marked elements of a unit whose rows are written, by the formula: a value
+// that is not finite decides its dim's sum whatever the finite ones are, so the
+// marks become the sums of those alone (an infinity times a weight of exactly
+// zero is NaN).  Thread (slot, chunk) walks the unit's slots for one head after
+// another.  Out of line, and with few arguments, so that the pass keeps its
+// registers (32 x 32K unchanged, 64 sequences of up to 300 tokens 26.0 -> 26.7
+// us; inline 27.0): reached only where there are such values.  All threads call.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgUnit<T, D>& u,
+__device__ __noinline__ void pg_not_finite(const PgDecodeIo& io, int unit, float* f) {
+    constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, ROWS = NT / CPR;
+    const int per = io.c.Hkv * io.c.nhb;
+    const PgUnit<T, D> u(io, PgSplit{0u, 0u, 0}, PgCursor{unit / per, unit % per, 0, 0u}, 1u);
+    const int chunk = threadIdx.x % CPR, row = threadIdx.x / CPR;
+    const T* K = static_cast<const T*>(io.c.k);
+    const T* V = static_cast<const T*>(io.c.v) + chunk * EPC;
+#pragma unroll 1
+    for (int h = 0; h < u.gh; ++h) {
+        const float sl = u.slope2(io, h);
+        float s[EPC];
+#pragma unroll
+        for (int j = 0; j < EPC; ++j) s[j] = 0.f;
+#pragma unroll 1
+        for (int y = row; y < u.ls.n; y += ROWS) {
+            float dist;
+            const long long off = pg_see(io, pg_fetch(io, u.ls, u.trow, u.prow, y, u.ls.n), u.prow != nullptr, u.g,
+                                         u.newest, dist);
+            if (off < 0) continue;
+            float v[EPC];
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < EPC; ++j) {
+                v[j] = to_f32<T>(V[off + j]);
+                v[j] = v[j] - v[j] == 0.f ? 0.f : v[j];            // infinities and NaN stay
+                odd |= v[j] != 0.f;
+            }
+            if (!odd) continue;
+            float dot = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < D; ++e) dot = fmaf(to_f32<T>(u.q[(size_t)h * D + e]), to_f32<T>(K[off + e]), dot);
+            const float w = pg_logit(io, pg_cap(io, dot), sl, dist, 0.f) == -INFINITY ? 0.f : 1.f;
+#pragma unroll
+            for (int j = 0; j < EPC; ++j)
+                if (v[j] != 0.f) s[j] += w * v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < EPC; ++j) f[row * D + chunk * EPC + j] = s[j];
+        __syncthreads();
+        float* out = io.out + (u.qh0 + h) * D;
+        for (int e = threadIdx.x; e < D; e += NT) {
+            if (__float_as_uint(out[e]) == kPgMark) {
+                float sum = 0.f;
+                for (int x = 0; x < ROWS; ++x) sum += f[x * D + e];
+                out[e] = sum == 0.f ? NAN : sum;                   // none: finite values whose sum has overflowed
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// after all have put: the unit's last CTA joins.  All threads call; f as pg_join,
+// and so the result, for the whole CTA.
+template <typename T, int D, int NT>
+__device__ __forceinline__ bool pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgUnit<T, D>& u,
                                            const PgPart<T, D>& part, float* f) {
-    if (part.whole) return;
+    if (part.whole) return false;
     const int first = (int)sp.owner(u.own0), n = (int)sp.owner(u.own0 + u.nt - 1) - first + 1;
     unsigned* cnt = io.cnt + u.index;
+    bool odd = false;
     if (last_cta_of_unit(cnt, n)) {
 #pragma unroll 1
-        for (int h0 = 0; h0 < u.gh; h0 += 8) {
-            pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f);
-            __syncthreads();
-        }
+        for (int h0 = 0; h0 < u.gh; h0 += 8)
+            odd |= __syncthreads_or(pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f));
         reset_counter(cnt);
     }
+    return odd;
 }
 
 // Moves the cursor from its unit, nt tiles long, to the next; t0 moves along.
@@ -146,6 +206,7 @@ struct PgTc {
     static constexpr int kAcc = kWarps * 4 * (D + 4);            // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
     static constexpr size_t kSmem = kRing + 4 * (size_t)kScratch;
+    static_assert(kThreads * 16 / (int)sizeof(T) <= kScratch, "pg_not_finite: a float for each element a CTA reads at once");
 };
 
 __device__ __forceinline__ void pg_cp16(uint32_t s, const void* g, bool ok) {
@@ -370,7 +431,7 @@ __device__ __forceinline__ int pg_dim(int mt, int r, int j) {
 
 template <typename T, int D, int HB>
 __global__ void __launch_bounds__(PgTc<T, D>::kThreads, 1)
-k_paged_decode(PgDecodeIo io) {
+k_paged_decode(const __grid_constant__ PgDecodeIo io) {
     using Tc = PgTc<T, D>;
     constexpr int S = Tc::kStages, MT = D / 16, NW = Tc::kWarps, NT = Tc::kThreads;
     constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, RPI = 32 / CPR;     // chunks per row, rows per copy instruction
@@ -452,6 +513,7 @@ k_paged_decode(PgDecodeIo io) {
                 }
             }
             // four heads at a time through the scratch
+            bool odd = false;
 #pragma unroll
             for (int hq = 0; hq < HB / 4; ++hq) {
 #pragma unroll
@@ -477,11 +539,12 @@ k_paged_decode(PgDecodeIo io) {
                         A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
                         L = fmaf(s_ml[w][h][1], f, L);
                     }
-                    part.put(io, done, h, e, A, M, L);
+                    part.put(io, done, h, e, A, M, L, odd);
                 }
-                __syncthreads();
+                odd = __syncthreads_or(odd);
             }
-            pg_hand_in<T, D, NT>(io, sp, done, part, scratch);
+            odd |= pg_hand_in<T, D, NT>(io, sp, done, part, scratch);
+            if (odd) pg_not_finite<T, D, NT>(io, done.index, scratch);
         }
         if (!more) break;
         __syncthreads();                                          // the scratch has been read

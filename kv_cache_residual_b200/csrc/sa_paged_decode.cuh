@@ -77,17 +77,31 @@ __device__ __forceinline__ void pg_write_lse(const PgDecodeIo& io, size_t qh, fl
 // 1 / L, and 0 where nothing is seen (out = A inv: one rounding more than A / L)
 __device__ __forceinline__ float pg_inv(float L) { return L == 0.f ? 0.f : 1.f / L; }
 
+// A row's element, its sum of values A times inv = pg_inv(L).  Matrix products of
+// parts make NaN of an infinite value (zero parts, the parts of an infinity, a
+// weight that underflows), so where the row's weights are numbers and the sum is
+// not, a mark is left for pg_not_finite and `odd` set.
+constexpr unsigned kPgMark = 0x7fc0a11fu;          // a NaN that no operation makes
+__device__ __forceinline__ float pg_element(float A, float inv, bool& odd) {
+    const float y = inv == 0.f ? 0.f : A * inv;
+    if (y == y || inv != inv) return y;
+    odd = true;
+    return __uint_as_float(kPgMark);
+}
+
 // The unit's last CTA joins its n records (fixed order) and writes the rows of
 // its gh <= 8 heads from h0 on.  Thread (column, part): a column is four dims of
 // a head, and the records are cut into as many parts as there are threads for;
 // a part's first records are on their way before the weights are known.
-// f: shared scratch of kPgJoinFloats floats.  All threads call.
+// f: shared scratch of kPgJoinFloats floats.  All threads call; true where one
+// left marks.
 constexpr int kPgJoin = 10;                // records of a part in flight
 // the heads' m and l, then [head][record] weights, then over them the parts' sums (a float4 per thread)
 constexpr int kPgJoinFloats = 8 * (kPgSlots + 2);
 
 template <int D, int NT>
-__device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
+__device__ __forceinline__ bool pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
+    bool odd = false;                          // this thread has left marks
     const int hu = io.c.hu, floats = hu * (2 + D);
     float* sM = f;
     float* sL = f + 8;
@@ -189,9 +203,12 @@ __device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, 
         }
         if (mine && (parts == 1 || part == 0)) {
             const float inv = sL[h];
-            *reinterpret_cast<float4*>(io.out + (qh0 + h) * D + e) = make_float4(A.x * inv, A.y * inv, A.z * inv, A.w * inv);
+            *reinterpret_cast<float4*>(io.out + (qh0 + h) * D + e) =
+                make_float4(pg_element(A.x, inv, odd), pg_element(A.y, inv, odd), pg_element(A.z, inv, odd),
+                            pg_element(A.w, inv, odd));
         }
     }
+    return odd;
 }
 
 }  // namespace sa

@@ -865,3 +865,50 @@ def test_decode_queries_that_are_not_numbers(lens, dtype, d, G):
         for g in range(c.Hkv):
             bad = any(x == b and h // G == g for x, h in rows)
             assert torch.equal(torch.isnan(wo[b, g]), live[b] & bad)
+
+
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 4), (BF, 64, 8), (BF, 128, 12), (F32, 128, 4), (F32, 64, 8), (F32, 64, 12)])
+@pytest.mark.parametrize("lens", [[200, 1, 64], [9000, 30], [40] * 200], ids=["short", "long", "many"])
+def test_decode_values_that_are_not_finite(lens, dtype, d, G):
+    """An infinity among the values of seen slots goes where the formula has it;
+    opposite ones, NaN, and a weight of zero times an infinity give NaN; no other
+    dim or unit changes.  Weights here are at least e^-40 of the largest."""
+    c = Case(lens, G=G, d=d, dtype=dtype, seed=140)
+    inf = float("inf")
+    base, _ = sa.paged_decode(c.q, c.cache())
+    want = base.clone()
+    r = np.random.default_rng(141)
+
+    def put(b, h, s, e, x, y, heads=slice(None)):
+        pg, row, _ = opaged.slot_pages(c.table_h[b], c.lens[b], c.page, c.n_pages)
+        c.v[int(pg[s]), h, int(row[s]), e] = x
+        want[b, h * G:(h + 1) * G][heads, e] = y
+
+    for b in range(0, len(lens), 1 if len(lens) < 10 else 17):
+        at = r.integers(0, c.lens[b], 8)
+        put(b, 0, at[0], 3, inf, inf)
+        put(b, 0, at[1], 4, -inf, -inf)
+        put(b, 1, at[2], d - 1, inf, inf)
+        put(b, 1, c.lens[b] - 1, 0, -inf, -inf)
+        put(b, 1, at[3], 9, float("nan"), float("nan"))
+        if c.lens[b] > 1:
+            put(b, 0, 0, 7, inf, inf)
+            put(b, 0, c.lens[b] - 1, 7, -inf, float("nan"))
+    out, lse = sa.paged_decode(c.q, c.cache())
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(nan=5.0, posinf=inf, neginf=-inf), want.nan_to_num(nan=5.0, posinf=inf, neginf=-inf))
+    # the first head's logit of slot 2 is -inf: its weight is 0, and 0 times an infinity NaN
+    if lens[0] > 2:
+        c.q[0, 0], c.q[0, 1:G] = 0.0, 0.0
+        c.q[0, 0, 0] = 1.0
+        c.q[0, 1:G, 1] = 1.0
+        pg, row, _ = opaged.slot_pages(c.table_h[0], c.lens[0], c.page, c.n_pages)
+        c.k[int(pg[2]), 0, int(row[2])] = 1.0
+        c.k[int(pg[2]), 0, int(row[2]), 0] = -3e38
+        c.v[int(pg[2]), 0, int(row[2]), 11] = inf
+        out, lse = sa.paged_decode(c.q, c.cache(), scale=1e4)
+        assert torch.isnan(out[0, 0, 11]) and torch.isfinite(lse[0, :G]).all()
+        # a query that is not a number keeps its whole row
+        c.q[0, 0, 0] = float("nan")
+        out, lse = sa.paged_decode(c.q, c.cache())
+        assert torch.isnan(out[0, 0]).all() and not torch.isnan(out[0, 1, 0])
