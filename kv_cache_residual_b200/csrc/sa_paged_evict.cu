@@ -29,7 +29,8 @@ namespace sa {
 constexpr int kEvThreads = 512;
 constexpr int kEvBins = 2048, kEvCoarse = 64;
 constexpr int kEvUn = 2;               // quads of slots a thread reads at once
-constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory
+constexpr int kEvKeys = 40 * 1024;     // most keys of a slice kept in shared memory,
+constexpr int kEvKeysTwo = 21 * 1024;  // and where two CTAs share an SM
 constexpr int kEvMoveThreads = 256;
 constexpr int kEvMoveUn = 4;           // rows a lane group reads at once
 
@@ -404,8 +405,14 @@ PagedEvictPlan paged_evict_plan(const PagedDims& d, int budget) {
     // resident at once (two per SM)
     p.cluster = 1;
     while (p.cluster < 8 && (long long)d.U() * p.cluster * 2 <= 148 * 2 && d.cap / p.cluster > 1024) p.cluster *= 2;
+    // Longer slices than two CTAs of an SM have room for keep their keys in the
+    // workspace, or the clusters above would come in two waves (32 units of 256K to
+    // 64K: 260 us, 227 with the keys there; 16 units 203 and 196).  In shared memory
+    // all the same: with CTAs on half the SMs at most (8 units of 256K: 107 us, 114
+    // in the workspace), and units of one CTA (256 of 32K to 16 less: 51.7, 53.0).
     const int slice = (cdiv(d.cap, p.cluster) + 31) & ~31;
-    p.near_keys = slice <= kEvKeys ? slice : 0;
+    const bool alone = p.cluster == 1 || d.U() * p.cluster * 2 <= 148;
+    p.near_keys = slice <= (alone ? kEvKeys : kEvKeysTwo) ? slice : 0;
     const int past = d.cap > budget ? d.cap - budget : 0;
     p.moves = past < budget ? past : budget;
     size_t off = 0;

@@ -912,3 +912,16 @@ def test_decode_values_that_are_not_finite(lens, dtype, d, G):
         c.q[0, 0, 0] = float("nan")
         out, lse = sa.paged_decode(c.q, c.cache())
         assert torch.isnan(out[0, 0]).all() and not torch.isnan(out[0, 1, 0])
+
+
+@pytest.mark.parametrize("B,tracked", [(16, False), (3, True)])
+def test_evict_keys_of_long_slices(B, tracked):
+    """Tables of 256K slots: the keys in the workspace, and in shared memory."""
+    r = np.random.default_rng(160)
+    lens = [int(x) for x in r.integers(100, 3000, B)]
+    lens[0], lens[-1] = 262144, 90001
+    c = Case(lens, Hkv=1, G=1, d=64, page=64, tracked=tracked, seed=161)
+    c.weight = (c.weight * 2000).floor()                # ties
+    _evict(c, 70000, 64, 128)
+    c.lengths[0] = 200003
+    _evict(c, 60001, 5, 2)

@@ -259,3 +259,17 @@ def test_factors_that_underflow_are_refused():
     cache = _cache(k=k, v=v, table=table, lengths=lengths)
     for kw in (dict(softcap=1e37), dict(scale=1e-6, softcap=1e38), dict(scale=1e-20, softcap=1e20)):
         assert _decode(cache=cache, params=_params(**kw), q=a, out=b, lse=c, ws=ws) == bad, kw
+
+
+@pytest.mark.parametrize("B,pages,keys", [(4, 4096, True), (2, 4096, True), (1, 4096, False), (4, 2048, False),
+                                          (32, 512, False), (16, 1024, True), (1, 8192, True)])
+def test_evict_clusters_are_resident(B, pages, keys):
+    """Clusters are as large as fit at once with two CTAs on an SM: slices with
+    more keys than half an SM's memory have them in the workspace, but where
+    there are few CTAs or one a unit.  Pages of 64, eight KV heads."""
+    sh = _shape(B=B, Hq=8, Hkv=8, page=64, max_pages=pages, n_pages=B * pages)
+    cap, budget = 64 * pages, 1000
+    n = sa._lib().sa_paged_workspace_size(ctypes.byref(sh), sa.OP_PAGED_EVICT, budget)
+    lists = 4 * 2 * 8 * B * min(budget, cap - budget)
+    least = -(-4 * 8 * B // 256) * 256 + -(-lists // 256) * 256
+    assert n == least + (4 * 8 * B * cap if keys else 0)
