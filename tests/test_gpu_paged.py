@@ -925,3 +925,177 @@ def test_evict_keys_of_long_slices(B, tracked):
     _evict(c, 70000, 64, 128)
     c.lengths[0] = 200003
     _evict(c, 60001, 5, 2)
+
+
+@pytest.mark.parametrize("page,cols", [(1, 301), (3, 101), (5, 67), (7, 43)])
+@pytest.mark.parametrize("tracked", [False, True])
+def test_odd_capacities(page, cols, tracked):
+    """Rows of pos and of the weights that do not begin on 16 bytes."""
+    c = Case([301, 1, 150, 0, 299], page=page, cols=cols, d=64, tracked=tracked, seed=170)
+    slopes = torch.exp2(-torch.arange(1, c.Hq + 1, device=_dev(), dtype=F32))
+    _decode(c, weights=True, softcap=9.0)
+    _decode(c, weights=True, sink=3, local=50, slopes=slopes)
+    for budget in (1, 50, 149, 298):
+        c = Case([301, 1, 150, 0, 299], page=page, cols=cols, d=64, tracked=tracked, seed=171)
+        _evict(c, budget, 1 if budget > 1 else 0, 0 if budget < 9 else 7)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_arrays_that_begin_anywhere(off):
+    """Weights, positions and lse on 4 bytes but not on 16."""
+    dev = _dev()
+    c = Case([320, 100, 3], tracked=True, cols=20, seed=172)
+    n = c.weight.numel()
+
+    def at(t, dtype=F32):
+        x = torch.zeros(t.numel() + 8, dtype=dtype, device=dev)[off:off + t.numel()].view(t.shape)
+        return x.copy_(t)
+
+    c.weight, c.pos = at(c.weight), at(c.pos, I32)
+    c.lengths, c.seen = at(c.lengths, I32), at(c.seen, I32)
+    c.table = at(c.table, I32)
+    assert c.weight.data_ptr() % 16 == 4 * off and n % 4 == 0
+    before = torch.full(c.weight.shape, -3.0, device=dev)
+    wo, lse = at(before), at(torch.zeros(c.B, c.Hq, device=dev))
+    out, _ = sa.paged_decode(c.q, c.cache(), weight=c.weight, weight_out=wo, lse=lse, sink=2, local=200)
+    _check_decode(c, out, lse, wo, c.weight, before, sink=2, local=200)
+    _evict(c, 64, 4, 8)
+    lo, w2, p2 = sa.paged_evict(c.cache(), c.weight, 64, 4, 8, weight_out=at(before), pos_out=at(c.pos, I32),
+                                lengths_out=at(c.lengths, I32))
+    # the rows have moved once already, the weights and positions are as they were: the same choice again
+    again = sa.paged_evict(c.cache(), c.weight, 64, 4, 8)
+    live = torch.arange(c.cap, device=dev) < lo[:, None, None]
+    assert torch.equal(lo, again[0]) and torch.equal(torch.where(live, p2, 0), again[2])
+    assert torch.equal(torch.where(live, w2, torch.zeros_like(w2)), again[1])
+
+
+@pytest.mark.parametrize("ldw", [320, 321, 324, 333])
+@pytest.mark.parametrize("tracked", [False, True])
+def test_longer_rows_of_slots(ldw, tracked):
+    """pos and the weights as parts of wider arrays (ldw), through the C calls; what
+    lies past the capacity is left as it was."""
+    import ctypes
+    dev, lib = _dev(), sa._lib()
+    c = Case([320, 0, 17, 319], cols=20, tracked=tracked, seed=173)
+    wide = lambda t, fill, dtype: torch.full((c.B, c.Hkv, ldw), fill, dtype=dtype, device=dev).index_copy_(
+        2, torch.arange(c.cap, device=dev), t)
+    w, wo = wide(c.weight, -5.0, F32), torch.full((c.B, c.Hkv, ldw), -3.0, device=dev)
+    pos = wide(c.pos, -8, I32) if tracked else None
+    cache = c.cache()
+    shape = sa.sa_paged_shape.from_buffer_copy(cache._for_heads(c.Hq))
+    shape.ldw = ldw
+    raw = sa.sa_paged_cache.from_buffer_copy(cache._c)
+    raw.pos = None if pos is None else pos.data_ptr()
+    sh, rc = ctypes.byref(shape), ctypes.byref(raw)
+    stream = torch.cuda.current_stream().cuda_stream
+    out, lse = torch.empty(c.B, c.Hq, c.d, device=dev), torch.empty(c.B, c.Hq, device=dev)
+    n = lib.sa_paged_workspace_size(sh, sa.OP_PAGED_DECODE, 1)
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+    p = sa.sa_paged_params(0.0, 0.0, 3, 100, None, w.data_ptr(), wo.data_ptr(), 0)
+    assert lib.sa_paged_decode(sh, rc, ctypes.byref(p), c.q.data_ptr(), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
+                               stream) == sa.SA_OK
+    torch.cuda.synchronize()
+    before = torch.full((c.B, c.Hkv, c.cap), -3.0, device=dev)
+    _check_decode(c, out, lse, wo[..., :c.cap], c.weight, before, sink=3, local=100)
+    assert torch.all(wo[..., c.cap:] == -3.0) and torch.all(w[..., c.cap:] == -5.0)
+
+    lo = torch.zeros(c.B, dtype=I32, device=dev)
+    po = torch.full((c.B, c.Hkv, ldw), -9, dtype=I32, device=dev)
+    wo.fill_(-3.0)
+    n = lib.sa_paged_workspace_size(sh, sa.OP_PAGED_EVICT, 40)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    assert lib.sa_paged_evict(sh, rc, w.data_ptr(), 40, 2, 5, lo.data_ptr(), wo.data_ptr(), po.data_ptr(), ws.data_ptr(), n,
+                              stream) == sa.SA_OK
+    torch.cuda.synchronize()
+    for b in range(c.B):
+        for h in range(c.Hkv):
+            L = c.lens[b]
+            at = np.arange(L) if pos is None else pos[b, h, :L].cpu().numpy()
+            newest = (L if c.seen is None else int(c.seen[b])) - 1
+            src = opaged.evict_unit(f64(w[b, h, :L]), at, newest, 40, 2, 5)
+            m = min(L, 40)
+            assert int(lo[b]) == m and po[b, h, :m].tolist() == at[src].tolist()
+            assert torch.equal(wo[b, h, :m], w[b, h, torch.from_numpy(src).to(dev)])
+            assert torch.all(po[b, h, m:] == -9) and torch.all(wo[b, h, m:] == -3.0)
+    new = torch.randn(c.B, c.Hkv, c.d, device=dev).to(BF)
+    c.lengths.clamp_(min=1)
+    w2 = w.clone()
+    assert lib.sa_paged_append(sh, rc, new.data_ptr(), new.data_ptr(), 0, 0, None, c.B, w2.data_ptr(), stream) == sa.SA_OK
+    torch.cuda.synchronize()
+    last = torch.zeros_like(w, dtype=torch.bool)
+    for b in range(c.B):
+        last[b, :, int(c.lengths[b]) - 1] = True
+    assert torch.equal(w2, torch.where(last, torch.zeros_like(w), w))
+
+
+@pytest.mark.parametrize("n", [700, 9000])
+def test_evict_more_protected_than_may_stay(n):
+    """Every slot claims the newest position: the largest weights stay, with ties,
+    with weights that are not numbers, and in place where none moves."""
+    for weights in ("rand", "ties", "nan"):
+        c = Case([n, 20, n // 2], Hkv=2, G=1, d=64, tracked=True, seed=174)
+        c.pos.copy_((c.seen - 1)[:, None, None].expand_as(c.pos))
+        if weights == "ties":
+            c.weight = (c.weight * 3).floor()
+        if weights == "nan":
+            c.weight[..., ::3] = float("nan")
+        for b in range(c.B):                            # a few are not protected, with the largest weights
+            c.pos[b, :, 3:n:97] = 0
+            c.weight[b, :, 3:n:97] = 100.0
+        _evict(c, 64, 0, 8)
+
+
+def test_scratch_grows_under_calls_in_flight():
+    """Calls that need ever more scratch, enqueued behind one another with no wait,
+    a captured one among them."""
+    dev = _dev()
+    cs = [Case([L, 37, L // 3], G=G, d=64, dtype=dt, seed=180 + i)
+          for i, (L, G, dt) in enumerate([(40, 1, BF), (900, 4, F32), (2000, 12, BF), (5000, 20, F32), (9000, 4, BF)])]
+    want = []
+    for c in cs:
+        wo = torch.zeros_like(c.weight)
+        want.append((*sa.paged_decode(c.q, c.cache(), weight=c.weight, weight_out=wo), wo))
+    stream = torch.cuda.Stream()
+    caches, wos = [c.cache() for c in cs], [torch.zeros_like(c.weight) for c in cs]
+    graph = torch.cuda.CUDAGraph()
+    wg = torch.zeros_like(cs[2].weight)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        og, lg = sa.paged_decode(cs[2].q, caches[2], weight=cs[2].weight, weight_out=wg)
+    torch.cuda.synchronize()
+    sa._PAGED_WS.pop((dev.index, stream.cuda_stream), None)
+    got = []
+    with torch.cuda.stream(stream):
+        for c, cache, wo in zip(cs, caches, wos):
+            got.append((*sa.paged_decode(c.q, cache, weight=c.weight, weight_out=wo), wo))
+            graph.replay()
+            out, _, _ = sa.paged_evict(caches[0], cs[0].weight, 16, 1, 1)
+        for c, cache, wo in zip(cs, caches, wos):
+            sa.paged_decode(c.q, cache, weight=c.weight, weight_out=torch.zeros_like(wo))
+    torch.cuda.synchronize()
+    for a, b in zip(got[1:] + [(og, lg, wg)], want[1:] + [want[2]]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_threads_on_streams_of_their_own():
+    import threading
+    c = Case([4000, 77, 900], G=8, d=64, seed=190)
+    cache = c.cache()
+    want = sa.paged_decode(c.q, cache, softcap=20.0)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        for _ in range(30):
+            o, l = sa.paged_decode(c.q, cache, softcap=20.0, stream=stream)
+            stream.synchronize()
+            if not (torch.equal(o, want[0]) and torch.equal(l, want[1])):
+                bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
