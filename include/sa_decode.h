@@ -559,8 +559,9 @@ SA_API sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cac
  * gives out = 0, lse = -inf and adds no weight.  q [B, Hq, d] in dtype.  Keys
  * and values of slots that are not seen are not read; of those seen,
  * infinities in keys and values count as the formula has them: a logit of -inf
- * has the weight 0, and its product with an infinite value is NaN; every other
- * weight is above 0, however small. */
+ * has the weight 0, and its product with an infinite value is NaN (but where out
+ * is written over q, which is then gone); every other weight is above 0, however
+ * small. */
 SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cache* cache,
                                  const sa_paged_params* params, const void* q, float* out, float* lse, void* ws,
                                  size_t ws_bytes, void* stream);

@@ -69,9 +69,9 @@ struct PgPart {
         : whole(u.tile == 0 && u.end == u.nt), rec(pg_rec(io.rec, io.c.hu * (2 + D), blockIdx.x, u.tile == 0)) {}
     // accumulator A of dim e of head h, mass L relative to 2^M; odd: as pg_element
     __device__ __forceinline__ void put(const PgDecodeIo& io, const PgUnit<T, D>& u, int h, int e, float A, float M,
-                                        float L, bool& odd) const {
+                                        float L, int* odd) const {
         if (whole) {
-            io.out[(u.qh0 + h) * D + e] = pg_element(A, pg_inv(L), odd);
+            io.out[(u.qh0 + h) * D + e] = pg_element(A, pg_inv(L), u.index, odd);
             if (e == 0) pg_write_lse(io, u.qh0 + h, M, L);
         } else {
             rec[2 * io.c.hu + h * D + e] = A;
@@ -80,81 +80,99 @@ struct PgPart {
     }
 };
 
-// The marked elements of a unit whose rows are written, by the formula: a value
-// that is not finite decides its dim's sum whatever the finite ones are, so the
-// marks become the sums of those alone (an infinity times a weight of exactly
-// zero is NaN).  Thread (slot, chunk) walks the unit's slots for one head after
-// another.  Out of line, and with few arguments, so that the pass keeps its
-// registers (32 x 32K unchanged, 64 sequences of up to 300 tokens 26.0 -> 26.7
-// us; inline 27.0): reached only where there are such values.  All threads call.
+// The marked elements of a unit, by the formula: a value that is not finite
+// decides its dim's sum whatever the finite ones are, so what matters is which
+// kinds of them a head's weights meet (an infinity times a weight of exactly zero
+// is NaN).  The lanes of a row read its value chunks, eight rows at once, and
+// where one is not finite the row's logits, a chunk each.
 template <typename T, int D, int NT>
-__device__ __noinline__ void pg_not_finite(const PgDecodeIo& io, int unit, float* f) {
-    constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, ROWS = NT / CPR;
+__device__ __forceinline__ void pg_not_finite(const PgDecodeIo& io, int unit, unsigned* kinds) {
+    constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, ROWS = NT / CPR, RPW = 32 / CPR, UN = 8;
+    constexpr unsigned kPos = 1u, kNeg = 2u, kNan = 4u;
     const int per = io.c.Hkv * io.c.nhb;
+    const int lane = threadIdx.x & 31, at = (lane % CPR) * EPC;
+    const T* K = static_cast<const T*>(io.c.k) + at;
+    const T* V = static_cast<const T*>(io.c.v) + at;
     const PgUnit<T, D> u(io, PgSplit{0u, 0u, 0}, PgCursor{unit / per, unit % per, 0, 0u}, 1u);
-    const int chunk = threadIdx.x % CPR, row = threadIdx.x / CPR;
-    const T* K = static_cast<const T*>(io.c.k);
-    const T* V = static_cast<const T*>(io.c.v) + chunk * EPC;
-#pragma unroll 1
-    for (int h = 0; h < u.gh; ++h) {
-        const float sl = u.slope2(io, h);
-        float s[EPC];
-#pragma unroll
-        for (int j = 0; j < EPC; ++j) s[j] = 0.f;
-#pragma unroll 1
-        for (int y = row; y < u.ls.n; y += ROWS) {
-            float dist;
-            const long long off = pg_see(io, pg_fetch(io, u.ls, u.trow, u.prow, y, u.ls.n), u.prow != nullptr, u.g,
-                                         u.newest, dist);
-            if (off < 0) continue;
-            float v[EPC];
-            bool odd = false;
-#pragma unroll
-            for (int j = 0; j < EPC; ++j) {
-                v[j] = to_f32<T>(V[off + j]);
-                v[j] = v[j] - v[j] == 0.f ? 0.f : v[j];            // infinities and NaN stay
-                odd |= v[j] != 0.f;
-            }
-            if (!odd) continue;
-            float dot = 0.f;
-#pragma unroll 1
-            for (int e = 0; e < D; ++e) dot = fmaf(to_f32<T>(u.q[(size_t)h * D + e]), to_f32<T>(K[off + e]), dot);
-            const float w = pg_logit(io, pg_cap(io, dot), sl, dist, 0.f) == -INFINITY ? 0.f : 1.f;
-#pragma unroll
-            for (int j = 0; j < EPC; ++j)
-                if (v[j] != 0.f) s[j] += w * v[j];
-        }
-#pragma unroll
-        for (int j = 0; j < EPC; ++j) f[row * D + chunk * EPC + j] = s[j];
-        __syncthreads();
-        float* out = io.out + (u.qh0 + h) * D;
-        for (int e = threadIdx.x; e < D; e += NT) {
-            if (__float_as_uint(out[e]) == kPgMark) {
-                float sum = 0.f;
-                for (int x = 0; x < ROWS; ++x) sum += f[x * D + e];
-                out[e] = sum == 0.f ? NAN : sum;                   // none: finite values whose sum has overflowed
-            }
-        }
-        __syncthreads();
+    float* out = io.out + u.qh0 * D;
+    bool marked = false;
+    for (int x = threadIdx.x; x < u.gh * D; x += NT) {
+        kinds[x] = 0u;
+        marked |= __float_as_uint(out[x]) == kPgMark;
     }
+    if (!__syncthreads_or(marked)) return;
+#pragma unroll 1
+    for (int y0 = (threadIdx.x >> 5) * RPW; y0 < u.ls.n; y0 += ROWS * UN) {        // the warp's rows
+        PgRaw raw[UN];
+        long long off[UN];
+        float dist[UN];
+        uint4 w[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+            raw[i] = pg_fetch(io, u.ls, u.trow, u.prow, y0 + i * ROWS + lane / CPR, u.ls.n);
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            off[i] = pg_see(io, raw[i], u.prow != nullptr, u.g, u.newest, dist[i]);
+            w[i] = off[i] >= 0 ? *reinterpret_cast<const uint4*>(V + off[i]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            float v[EPC], a[EPC], k[EPC];
+            bool odd = false;
+            unpack<T>(w[i], v);
+#pragma unroll
+            for (int j = 0; j < EPC; ++j) odd |= !(fabsf(v[j]) < INFINITY);
+            if (!__any_sync(0xffffffffu, odd)) continue;
+            unpack<T>(off[i] >= 0 ? *reinterpret_cast<const uint4*>(K + off[i]) : make_uint4(0u, 0u, 0u, 0u), k);
+#pragma unroll 1
+            for (int h = 0; h < u.gh; ++h) {
+                unpack<T>(__ldg(reinterpret_cast<const uint4*>(u.q + (size_t)h * D + at)), a);
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < EPC; ++j) dot = fmaf(a[j], k[j], dot);
+                dot = group_sum<CPR>(dot);
+                const bool none = pg_logit(io, pg_cap(io, dot), u.slope2(io, h), dist[i], 0.f) == -INFINITY;
+#pragma unroll
+                for (int j = 0; j < EPC; ++j)
+                    if (!(fabsf(v[j]) < INFINITY))
+                        atomicOr(kinds + h * D + at + j, none || v[j] != v[j] ? kNan : v[j] > 0.f ? kPos : kNeg);
+            }
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < u.gh * D; x += NT) {
+        if (__float_as_uint(out[x]) == kPgMark)        // no kind: finite values whose sum has overflowed
+            out[x] = kinds[x] == kPos ? INFINITY : kinds[x] == kNeg ? -INFINITY : NAN;
+    }
+    __syncthreads();
 }
 
-// after all have put: the unit's last CTA joins.  All threads call; f as pg_join,
-// and so the result, for the whole CTA.
+// The same for units [first, last]: this CTA has written both, and so all between,
+// which lie whole in its range.  Called at the CTA's end, out of line, so that the
+// pass keeps its registers: it and the elements' check cost short units
+// a little and long ones nothing (64 sequences of up to 300 tokens 25.7 -> 26.4 us,
+// 32 x 32K 674); one infinity in 128K slots takes 2.6 ms.  All threads call.
 template <typename T, int D, int NT>
-__device__ __forceinline__ bool pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgUnit<T, D>& u,
-                                           const PgPart<T, D>& part, float* f) {
-    if (part.whole) return false;
+__device__ __noinline__ void pg_marked(const PgDecodeIo& io, int first, int last, unsigned* kinds) {
+#pragma unroll 1
+    for (int unit = first; unit <= last; ++unit) pg_not_finite<T, D, NT>(io, unit, kinds);
+}
+
+// after all have put: the unit's last CTA joins.  All threads call; f, odd as pg_join.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void pg_hand_in(const PgDecodeIo& io, const PgSplit& sp, const PgUnit<T, D>& u,
+                                           const PgPart<T, D>& part, float* f, int* odd) {
+    if (part.whole) return;
     const int first = (int)sp.owner(u.own0), n = (int)sp.owner(u.own0 + u.nt - 1) - first + 1;
     unsigned* cnt = io.cnt + u.index;
-    bool odd = false;
     if (last_cta_of_unit(cnt, n)) {
 #pragma unroll 1
-        for (int h0 = 0; h0 < u.gh; h0 += 8)
-            odd |= __syncthreads_or(pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f));
+        for (int h0 = 0; h0 < u.gh; h0 += 8) {
+            pg_join<D, NT>(io, first, n, u.qh0 + h0, h0, min(8, u.gh - h0), f, u.index, odd);
+            __syncthreads();
+        }
         reset_counter(cnt);
     }
-    return odd;
 }
 
 // Moves the cursor from its unit, nt tiles long, to the next; t0 moves along.
@@ -212,7 +230,7 @@ struct PgTc {
     static constexpr int kAcc = kWarps * 4 * (D + 4);            // floats: four heads' states of the warps
     static constexpr int kScratch = kAcc > kPgJoinFloats ? kAcc : kPgJoinFloats;
     static constexpr size_t kSmem = kRing + 4 * (size_t)kScratch;
-    static_assert(kThreads * 16 / (int)sizeof(T) <= kScratch, "pg_not_finite: a float for each element a CTA reads at once");
+    static_assert((kBf16 ? 16 : 8) * D <= kScratch, "pg_not_finite: a word for each element of a unit");
 };
 
 __device__ __forceinline__ void pg_cp16(uint32_t s, const void* g, bool ok) {
@@ -445,6 +463,7 @@ k_paged_decode(const __grid_constant__ PgDecodeIo io) {
     constexpr int LD = D + 4;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float s_ml[NW][HB][2];
+    __shared__ int s_odd[2];                                     // the first and the last unit with marks
     const PagedView& c = io.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, t = lane & 3;
     unsigned char* ring = smem + warp * S * Tc::kBytes;
@@ -455,6 +474,7 @@ k_paged_decode(const __grid_constant__ PgDecodeIo io) {
     PgSplit sp;
     PgCursor cur;
     unsigned t0, t1;
+    if (threadIdx.x == 0) { s_odd[0] = 0x7fffffff; s_odd[1] = -1; }
     cudaTriggerProgrammaticLaunchCompletion();                   // the weights' kernel may come and wait
     if (!pg_locate<NT>(c.B, c.Hkv * c.nhb, io.extra, blockIdx.x, SA_PG_TILES(io), sp, cur, t0, t1)) return;
 
@@ -519,7 +539,6 @@ k_paged_decode(const __grid_constant__ PgDecodeIo io) {
                 }
             }
             // four heads at a time through the scratch
-            bool odd = false;
 #pragma unroll
             for (int hq = 0; hq < HB / 4; ++hq) {
 #pragma unroll
@@ -545,12 +564,11 @@ k_paged_decode(const __grid_constant__ PgDecodeIo io) {
                         A = fmaf(scratch[(w * 4 + h4) * LD + e], f, A);
                         L = fmaf(s_ml[w][h][1], f, L);
                     }
-                    part.put(io, done, h, e, A, M, L, odd);
+                    part.put(io, done, h, e, A, M, L, s_odd);
                 }
-                odd = __syncthreads_or(odd);
+                __syncthreads();
             }
-            odd |= pg_hand_in<T, D, NT>(io, sp, done, part, scratch);
-            if (odd) pg_not_finite<T, D, NT>(io, done.index, scratch);
+            pg_hand_in<T, D, NT>(io, sp, done, part, scratch, s_odd);
         }
         if (!more) break;
         __syncthreads();                                          // the scratch has been read
@@ -659,6 +677,8 @@ k_paged_decode(const __grid_constant__ PgDecodeIo io) {
         if (more) u = next;
     }
     tc::cp_wait<0>();
+    __syncthreads();
+    if (s_odd[1] >= 0) pg_marked<T, D, NT>(io, s_odd[0], s_odd[1], reinterpret_cast<unsigned*>(scratch));
 }
 
 // weight_out = weight + the step's attention weights summed over the group's

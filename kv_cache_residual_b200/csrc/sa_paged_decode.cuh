@@ -80,12 +80,16 @@ __device__ __forceinline__ float pg_inv(float L) { return L == 0.f ? 0.f : 1.f /
 // A row's element, its sum of values A times inv = pg_inv(L).  Matrix products of
 // parts make NaN of an infinite value (zero parts, the parts of an infinity, a
 // weight that underflows), so where the row's weights are numbers and the sum is
-// not, a mark is left for pg_not_finite and `odd` set.
+// not, a mark is left for pg_not_finite, and the unit noted in `odd` (shared: the
+// first and the last).
 constexpr unsigned kPgMark = 0x7fc0a11fu;          // a NaN that no operation makes
-__device__ __forceinline__ float pg_element(float A, float inv, bool& odd) {
-    const float y = inv == 0.f ? 0.f : A * inv;
-    if (y == y || inv != inv) return y;
-    odd = true;
+__device__ __forceinline__ float pg_element(float A, float inv, int unit, int* odd) {
+    const float y = A * inv;
+    if (y == y) return y;
+    if (inv == 0.f) return 0.f;                    // nothing seen, or every weight 0
+    if (inv != inv) return y;
+    atomicMin(odd, unit);
+    atomicMax(odd + 1, unit);
     return __uint_as_float(kPgMark);
 }
 
@@ -93,15 +97,15 @@ __device__ __forceinline__ float pg_element(float A, float inv, bool& odd) {
 // its gh <= 8 heads from h0 on.  Thread (column, part): a column is four dims of
 // a head, and the records are cut into as many parts as there are threads for;
 // a part's first records are on their way before the weights are known.
-// f: shared scratch of kPgJoinFloats floats.  All threads call; true where one
-// left marks.
+// f: shared scratch of kPgJoinFloats floats; unit, odd: as pg_element.  All threads
+// call.
 constexpr int kPgJoin = 10;                // records of a part in flight
 // the heads' m and l, then [head][record] weights, then over them the parts' sums (a float4 per thread)
 constexpr int kPgJoinFloats = 8 * (kPgSlots + 2);
 
 template <int D, int NT>
-__device__ __forceinline__ bool pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f) {
-    bool odd = false;                          // this thread has left marks
+__device__ __forceinline__ void pg_join(const PgDecodeIo& io, int first, int n, size_t qh0, int h0, int gh, float* f,
+                                        int unit, int* odd) {
     const int hu = io.c.hu, floats = hu * (2 + D);
     float* sM = f;
     float* sL = f + 8;
@@ -204,11 +208,10 @@ __device__ __forceinline__ bool pg_join(const PgDecodeIo& io, int first, int n, 
         if (mine && (parts == 1 || part == 0)) {
             const float inv = sL[h];
             *reinterpret_cast<float4*>(io.out + (qh0 + h) * D + e) =
-                make_float4(pg_element(A.x, inv, odd), pg_element(A.y, inv, odd), pg_element(A.z, inv, odd),
-                            pg_element(A.w, inv, odd));
+                make_float4(pg_element(A.x, inv, unit, odd), pg_element(A.y, inv, unit, odd),
+                            pg_element(A.z, inv, unit, odd), pg_element(A.w, inv, unit, odd));
         }
     }
-    return odd;
 }
 
 }  // namespace sa
