@@ -529,7 +529,9 @@ typedef struct {
 } sa_paged_params;
 
 /* Bytes of scratch of sa_paged_decode (arg != 0: with weight_out) or
- * sa_paged_evict (arg = budget).  0 on invalid arguments.  Of the decode's only
+ * sa_paged_evict (arg = budget).  0 on invalid arguments.  It follows the table's
+ * width, not the lengths: with weight_out the decode keeps a logit for every
+ * query head and slot of the capacity, 4 B Hq cap bytes.  Of the decode's only
  * the first 4 B Hkv ceil(Hq / (8 Hkv)) bytes (the completion tickets) have to
  * be zero when it is first used; the eviction's need not be.  A workspace
  * serves one shape and one call at a time: calls that may run side by side
@@ -546,7 +548,8 @@ SA_API size_t sa_paged_workspace_size(const sa_paged_shape* shape, int op, int a
  * seen[b] - n_b + i.  pos (when not NULL) and weight (when not NULL,
  * [B, Hkv, ldw] f32: set to 0) of those slots are written for every head.
  * Tokens outside [start[0], start[B]), slots outside [0, cap) and pages
- * outside the pool are skipped.  No workspace; one kernel. */
+ * outside the pool are skipped.  A length past cap counts as cap: its newest
+ * tokens go over what the last slots hold.  No workspace; one kernel. */
 SA_API sa_status sa_paged_append(const sa_paged_shape* shape, const sa_paged_cache* cache, const void* k_new,
                                  const void* v_new, long long token_stride, long long head_stride,
                                  const int32_t* start, int n_new, float* weight, void* stream);
@@ -578,7 +581,10 @@ SA_API sa_status sa_paged_decode(const sa_paged_shape* shape, const sa_paged_cac
  * (weight_out f32, pos_out int32, both [B, Hkv, ldw]; past it they are left as
  * they were).  The outputs lie apart from the inputs: repeating a call
  * on the same inputs gives the same result.  A sequence's pages must be its
- * own, each in one place of the table: rows are moved in place.  Pass the
+ * own, each in one place of the table: rows are moved in place, and nothing can
+ * tell a page that two sequences share.  Rows on pages that are not the pool's
+ * do not move: where one should have, the slot keeps the rows it had, so weed
+ * such entries out of the table before.  Pass the
  * outputs as the cache's lengths, pos and weights from then on. */
 SA_API sa_status sa_paged_evict(const sa_paged_shape* shape, const sa_paged_cache* cache, const float* weight,
                                 int budget, int sink, int local, int32_t* lengths_out, float* weight_out,

@@ -763,7 +763,9 @@ def paged_evict(cache, weight, budget, sink=0, local=0, lengths_out=None, weight
         cache = PagedCache(cache.k, cache.v, cache.table, lengths, pos, seen)
 
     where seen counts the tokens each sequence ever had (before the first
-    eviction: the old lengths).  The pages past the new lengths are free."""
+    eviction: the old lengths).  The pages past the new lengths are free.  Every
+    page has to be in one place of the table: one that two sequences share (a
+    common prefix) would be thinned out for both."""
     weight = _dense(weight, "weight", torch.float32, cache.slots, cache.device)
     _need(0 < budget < 2 ** 31, "budget must be a positive int32")
     _need(-1 < sink < 2 ** 31 and -1 < local < 2 ** 31, "sink and local must be int32, not negative")
