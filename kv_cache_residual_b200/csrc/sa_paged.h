@@ -56,9 +56,12 @@ struct PagedDecodePlan {
     size_t off_cnt, off_rec, off_lse, off_x, bytes;
 };
 
-// What a CTA spends on a unit beside its tiles is about the time of 128 KB
-// (48 ragged, windowed sequences: 77 us without, 69 / 63 / 60 / 61 us with
-// 32 / 64 / 128 / 192 KB).
+// What a CTA spends on a unit beside its tiles is about the time of 128 KB.  In
+// us with 0 / 32 / 64 / 128 / 192 / 256 KB: 48 ragged windowed sequences, heads of
+// 64: 65 / 58 / 53 / 52 / 52 / 54; 256 of 3..300 tokens: 104 / 82 / 77 / 75 / 75 /
+// 77; 32 of 100..8K: 114 / 107 / 104 / 100 / 100 / 101; fp32, 64 of 20..4K: 299 /
+// 300 / 285 / 273 / 274 / 277; 16 of 50..16K, 16 heads a group: 45 / 44 / 44 / 41 /
+// 41 / 40; 1 x 32K: 38 / 38 / 37 / 36 / 34 / 34.
 inline int paged_extra(const PagedDims& d) { return (1 << 17) / (2 * kPgTile * d.d * d.esz()); }
 
 inline PagedDecodePlan paged_decode_plan(const PagedDims& d, bool weights) {
