@@ -1099,3 +1099,55 @@ def test_threads_on_streams_of_their_own():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n_pages,Hkv,page", [(1, 1, 1), (1, 1, 48), (40, 1, 1), (1, 3, 48), (40, 3, 1), (3, 1, 16)])
+def test_dims_of_one(n_pages, Hkv, page, dtype):
+    """A pool's, a batch's and a call's dims of size one, whose strides mean nothing."""
+    dev, d, G = _dev(), 64, 2
+    n = min(n_pages, 40) * page
+    st = [7 if n_pages == 1 else Hkv * page * d + 64, 3 if Hkv == 1 else page * d, 5 if page == 1 else d, 1]
+    size = (n_pages, Hkv, page, d)
+    store = [torch.full((2 ** 16 * 4,), float("nan"), dtype=dtype, device=dev) for _ in range(2)]
+    k, v = (torch.as_strided(t, size, st) for t in store)
+    table = torch.arange(n_pages, dtype=I32, device=dev).flip(0)[None].contiguous()
+    lengths = torch.tensor([n], dtype=I32, device=dev)
+    cache = sa.PagedCache(k, v, table, lengths)
+    g = torch.Generator(device="cuda").manual_seed(200)
+    kn, vn = (torch.randn(n, Hkv, d, generator=g, device=dev).to(dtype) for _ in range(2))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    sa.paged_append(cache, kn[:n - 1], vn[:n - 1], start=torch.tensor([1, n], dtype=I32, device=dev)) if n > 1 else None
+    lengths.fill_(n - 1)
+    torch.cuda.synchronize()
+    # n - 1 tokens one place on: the first was skipped; write all in their places, the last one alone
+    if n > 1:
+        sa.paged_append(cache, kn[:n - 1], vn[:n - 1], start=torch.tensor([0, n - 1], dtype=I32, device=dev), stream=stream)
+    stream.synchronize()
+    lengths.fill_(n)
+    torch.cuda.synchronize()
+    last = [torch.as_strided(t[n - 1:].contiguous(), (1, Hkv, d), (9, 11 if Hkv == 1 else d, 1)) for t in (kn, vn)]
+    sa.paged_append(cache, *last, stream=stream)
+    stream.synchronize()
+    q = torch.randn(1, Hkv * G, d, generator=g, device=dev).to(dtype)
+    q1 = torch.as_strided(q, q.shape, (13, d, 1))
+    out, lse = sa.paged_decode(q1, cache)
+    for h in range(Hkv):
+        ro, rl, _ = opaged.decode_unit(f64(q[0, h * G:(h + 1) * G]), f64(kn[:, h]), f64(vn[:, h]), np.arange(n), n - 1,
+                                       np.ones(n, dtype=bool), d ** -0.5)
+        # logits below 8 and values below 6, the bound of the module's head: well below 1e-4
+        assert np.abs(f64(out[0, h * G:(h + 1) * G]) - ro).max() < 1e-4
+        assert np.abs(f64(lse[0, h * G:(h + 1) * G]) - rl).max() < 1e-4
+    w = torch.rand(cache.slots, generator=g, device=dev)
+    budget = max(1, n // 3)
+    torch.cuda.synchronize()
+    kept, w2, p2 = sa.paged_evict(cache, w, budget, stream=stream)
+    stream.synchronize()
+    assert kept.tolist() == [budget]
+    for h in range(Hkv):
+        src = opaged.evict_unit(f64(w[0, h]), np.arange(n), n - 1, budget, 0, 0)
+        assert p2[0, h, :budget].tolist() == src.tolist()
+        pg, row, _ = opaged.slot_pages(table.cpu().numpy()[0], budget, page, n_pages)
+        assert torch.equal(k[pg, h, row], kn[torch.from_numpy(src).to(dev), h])
+        assert torch.equal(v[pg, h, row], vn[torch.from_numpy(src).to(dev), h])
